@@ -37,6 +37,10 @@ PAIRING_HALF = 0
 PAIRING_INTERLEAVED = 1
 DTYPE_FP16 = 0
 DTYPE_FP32 = 1
+ROPE_PLAIN = 0
+ROPE_LINEAR = 1
+ROPE_LLAMA3 = 2
+ROPE_YARN = 3
 TILE_TOKENS = 64
 TAG_KEY = 0x4B
 TAG_VALUE = 0x56
@@ -47,6 +51,8 @@ ABI_FUNCTIONS = (
     "gtq_strerror", "gtq_last_error", "gtq_lloyd_max", "gtq_rotation", "gtq_layout_tile_bytes",
     "gtq_block_energy_noalloc", "gtq_plan_device_bytes", "gtq_raise_status",
     "gtq_alloc_bits_ex", "gtq_quantize_pack_ex", "gtq_decode_attn_ex", "gtq_decode_attn_full",
+    "gtq_rope", "gtq_chunk_attn", "gtq_chunk_workspace_bytes", "gtq_attn_weights",
+    "gtq_weights_workspace_bytes", "gtq_evict", "gtq_evict_workspace_bytes",
 )
 
 
@@ -120,6 +126,51 @@ def fp16_kv(v=None, recent_k=None, recent_v=None, recent_lens=None, recent_len=N
     return kv
 
 
+class gtq_rope_config(ctypes.Structure):
+    _fields_ = [
+        ("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+        ("rope_pairing", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("scaling", ctypes.c_int32), ("backward", ctypes.c_int32),
+        ("theta", ctypes.c_double), ("factor", ctypes.c_double),
+        ("original_context", ctypes.c_double), ("low_freq", ctypes.c_double),
+        ("high_freq", ctypes.c_double), ("magnitude", ctypes.c_double),
+    ]
+
+
+class gtq_rope_tensor(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int32),
+        ("reserved", ctypes.c_int32), ("x_strides", ctypes.c_int64 * 4),
+        ("y_strides", ctypes.c_int64 * 4),
+    ]
+
+
+class gtq_chunk(ctypes.Structure):
+    _fields_ = [
+        ("n_tokens", ctypes.c_int64), ("chunk_lens_dev", ctypes.c_void_p),
+        ("causal", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("q_strides", ctypes.c_int64 * 4), ("out_strides", ctypes.c_int64 * 4),
+    ]
+
+
+class gtq_eviction(ctypes.Structure):
+    _fields_ = [
+        ("keep", ctypes.c_int64), ("n_first", ctypes.c_int64), ("n_recent", ctypes.c_int64),
+        ("weights_dev", ctypes.c_void_p), ("w_strides", ctypes.c_int64 * 2),
+        ("weights_out_dev", ctypes.c_void_p), ("w_out_strides", ctypes.c_int64 * 2),
+        ("kept_dev", ctypes.c_void_p), ("new_lens_dev", ctypes.c_void_p),
+    ]
+
+
+def make_rope(head_dim, theta, rotary_dim=None, rope_pairing=PAIRING_HALF, dtype=DTYPE_FP16,
+              scaling=ROPE_PLAIN, factor=1.0, original_context=0.0, low_freq=1.0, high_freq=4.0,
+              magnitude=1.0, backward=False) -> gtq_rope_config:
+    """A gtq_rope_config; rotary_dim defaults to the whole head."""
+    return gtq_rope_config(head_dim, head_dim if rotary_dim is None else rotary_dim, rope_pairing,
+                           dtype, scaling, int(backward), theta, factor, original_context,
+                           low_freq, high_freq, magnitude)
+
+
 def make_config(batch, n_q_heads, n_kv_heads, k_bits, v_bits, t_capacity, head_dim=128,
                 max_bits=8, rope_pairing=PAIRING_HALF, in_dtype=DTYPE_FP16, seed=0) -> gtq_config:
     return gtq_config(batch, n_q_heads, n_kv_heads, head_dim, k_bits, v_bits, max_bits,
@@ -158,6 +209,18 @@ def _load():
         "gtq_decode_attn_ex": (I32, [P, P, I64, ctypes.POINTER(gtq_seq_layout), P, I32, P, P]),
         "gtq_decode_attn_full": (I32, [P, P, I64, ctypes.POINTER(gtq_seq_layout),
                                        ctypes.POINTER(gtq_fp16_kv), P, I32, P, P]),
+        "gtq_rope": (I32, [ctypes.POINTER(gtq_rope_config), I64, I64, P, I64, I64,
+                           ctypes.POINTER(gtq_rope_tensor), ctypes.POINTER(gtq_rope_tensor), P]),
+        "gtq_chunk_attn": (I32, [P, P, I64, ctypes.POINTER(gtq_seq_layout),
+                                 ctypes.POINTER(gtq_chunk), P, P, P, SZ, P]),
+        "gtq_chunk_workspace_bytes": (SZ, [P, I64, I64]),
+        "gtq_attn_weights": (I32, [P, P, I64, ctypes.POINTER(gtq_seq_layout),
+                                   ctypes.POINTER(gtq_chunk), P, P, P, I64x4, P, SZ, P]),
+        "gtq_weights_workspace_bytes": (SZ, [P, I64, I64]),
+        "gtq_evict": (I32, [P, P, I64, ctypes.POINTER(gtq_seq_layout),
+                            ctypes.POINTER(gtq_eviction), P, SZ, ctypes.POINTER(gtq_seq_layout),
+                            P, SZ, P]),
+        "gtq_evict_workspace_bytes": (SZ, [P, I64]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -314,6 +377,143 @@ def gtq_decode_attn_full(plan: Plan, packed, T: int, q, out, layout=None, kv=Non
                                    None if kv is None else ctypes.byref(kv), _ptr(q),
                                    int(q_dtype), _ptr(out), _stream(stream))
     _check(rc, "gtq_decode_attn_full")
+
+
+def _rope_tensor(cfg, x, y, batch, tokens, name):
+    if y is None:
+        y = x
+    if x.dim() != 4 or tuple(x.shape) != tuple(y.shape):
+        raise ValueError("%s and its output must be 4-D [batch, heads, tokens, head_dim] of one shape" % name)
+    if x.shape[3] != cfg.head_dim or x.shape[0] != batch or x.shape[2] != tokens:
+        raise ValueError("%s must be [%d, heads, %d, %d]" % (name, batch, tokens, cfg.head_dim))
+    if x.element_size() != (2 if cfg.dtype == DTYPE_FP16 else 4) or y.dtype != x.dtype:
+        raise ValueError("%s and its output must have the config's dtype" % name)
+    return gtq_rope_tensor(_ptr(x), _ptr(y), int(x.shape[1]), 0, _strides4(x, None),
+                           _strides4(y, None))
+
+
+def gtq_rope(cfg: gtq_rope_config, q=None, q_out=None, k=None, k_out=None, positions=None, pos0=0,
+             stream=None) -> None:
+    """Rotate q and / or k ([batch, heads, tokens, head_dim], any strides with a dense last dim)
+    into q_out / k_out (None: in place).  positions: int64 [batch, tokens] or [tokens], or None:
+    pos0 + token."""
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("gtq_rope needs q or k")
+    batch, tokens = int(first.shape[0]), int(first.shape[2])
+    pos_stride = 0
+    if positions is not None:
+        if positions.element_size() != 8 or positions.shape[-1] != tokens or (
+                positions.dim() == 2 and positions.shape[0] != batch) or positions.dim() > 2:
+            raise ValueError("positions must be int64 [batch, tokens] or [tokens]")
+        if tokens > 1 and positions.stride(-1) != 1:
+            raise ValueError("positions must be dense along tokens")
+        pos_stride = int(positions.stride(0)) if positions.dim() == 2 and batch > 1 else 0
+    tq = None if q is None else _rope_tensor(cfg, q, q_out, batch, tokens, "q")
+    tk = None if k is None else _rope_tensor(cfg, k, k_out, batch, tokens, "k")
+    rc = _lib.gtq_rope(ctypes.byref(cfg), batch, tokens, _ptr(positions), pos_stride, int(pos0),
+                       None if tq is None else ctypes.byref(tq),
+                       None if tk is None else ctypes.byref(tk), _stream(stream))
+    _check(rc, "gtq_rope")
+
+
+def _chunk(plan, q, out, chunk_lens, causal):
+    c = plan.cfg
+    if q.dim() != 4 or q.element_size() != 2 or q.shape[0] != c.batch or (
+            q.shape[1] != c.n_q_heads or q.shape[3] != c.head_dim):
+        raise ValueError("q must be fp16 [batch, query heads, new tokens, %d]" % c.head_dim)
+    if out is not None and (tuple(out.shape) != tuple(q.shape) or out.dtype != q.dtype):
+        raise ValueError("out must have the shape and type of q")
+    ch = gtq_chunk(int(q.shape[2]), _ptr(chunk_lens) or None, int(bool(causal)), 0)
+    ch.q_strides = _live_strides(q)
+    ch.out_strides = _live_strides(out if out is not None else q)
+    return ch
+
+
+def _live_strides(x):
+    """Strides with 0 for dims of one element, whose stride says nothing."""
+    return (ctypes.c_int64 * 4)(*[int(s) if n > 1 else 0 for n, s in zip(x.shape[:3], x.stride()[:3])],
+                                int(x.stride(3)))
+
+
+def _nbytes(x) -> int:
+    return int(x.numel() * x.element_size())
+
+
+def gtq_chunk_workspace(plan: Plan, T: int, n_tokens: int) -> int:
+    """Bytes of the workspace gtq_chunk_attn needs for these sizes."""
+    return int(_lib.gtq_chunk_workspace_bytes(plan.handle, int(T), int(n_tokens)))
+
+
+def gtq_chunk_attn(plan: Plan, packed, T: int, q, out, workspace, layout=None, chunk_lens=None,
+                   causal=True, stream=None) -> None:
+    """Attention of the new tokens q [batch, query heads, new tokens, 128] (fp16, any strides with
+    dense rows) over the cache into out (the same shape)."""
+    ch = _chunk(plan, q, out, chunk_lens, causal)
+    rc = _lib.gtq_chunk_attn(plan.handle, _ptr(packed), int(T), _lay(layout), ctypes.byref(ch),
+                             _ptr(q), _ptr(out), _ptr(workspace), _nbytes(workspace),
+                             _stream(stream))
+    _check(rc, "gtq_chunk_attn")
+
+
+def gtq_weights_workspace(plan: Plan, T: int, n_tokens: int) -> int:
+    """Bytes of the workspace gtq_attn_weights needs for these sizes."""
+    return int(_lib.gtq_weights_workspace_bytes(plan.handle, int(T), int(n_tokens)))
+
+
+def _weights2(w, plan, what):
+    if w.dim() != 3 or w.element_size() != 4 or tuple(w.shape[:2]) != (plan.cfg.batch, plan.cfg.n_kv_heads):
+        raise ValueError("%s must be fp32 [batch, kv heads, tokens]" % what)
+    if w.shape[2] > 1 and w.stride(2) != 1:
+        raise ValueError("%s must be dense along tokens" % what)
+    return (ctypes.c_int64 * 2)(int(w.stride(0)), int(w.stride(1)))
+
+
+def gtq_attn_weights(plan: Plan, packed, T: int, q, weights_out, workspace, weights_in=None,
+                     layout=None, chunk_lens=None, causal=True, stream=None) -> None:
+    """weights_out = weights_in (or 0) + the attention every cached token gets from q; both
+    [batch, kv heads, >= T] fp32."""
+    ch = _chunk(plan, q, None, chunk_lens, causal)
+    st = _weights2(weights_out, plan, "weights_out")
+    if weights_out.shape[2] < T or (weights_in is not None and (
+            weights_in.shape[2] < T or tuple(_weights2(weights_in, plan, "weights_in")) != tuple(st))):
+        raise ValueError("weights_in and weights_out need T tokens and the same strides")
+    rc = _lib.gtq_attn_weights(plan.handle, _ptr(packed), int(T), _lay(layout), ctypes.byref(ch),
+                               _ptr(q), _ptr(weights_in), _ptr(weights_out), st, _ptr(workspace),
+                               _nbytes(workspace), _stream(stream))
+    _check(rc, "gtq_attn_weights")
+
+
+def gtq_evict_workspace(plan: Plan, T: int) -> int:
+    """Bytes of the workspace gtq_evict needs for caches of up to T tokens a sequence."""
+    return int(_lib.gtq_evict_workspace_bytes(plan.handle, int(T)))
+
+
+def gtq_evict(plan: Plan, packed, T: int, weights, keep: int, dst, new_lens, workspace, n_first=0,
+              n_recent=0, layout=None, dst_layout=None, weights_out=None, kept=None,
+              stream=None) -> None:
+    """Move the tokens that stay (n_first, n_recent, and the largest weights) into dst.
+    weights [batch, kv heads, >= T]; weights_out [batch, kv heads, >= keep]; kept int32
+    [batch, kv heads, keep]; new_lens int32 [batch]."""
+    c = plan.cfg
+    if weights.shape[2] < T or (weights_out is not None and weights_out.shape[2] < min(keep, T)):
+        raise ValueError("weights need T tokens, weights_out min(keep, T)")
+    if kept is not None and (tuple(kept.shape) != (c.batch, c.n_kv_heads, keep) or not kept.is_contiguous()
+                             or kept.element_size() != 4):
+        raise ValueError("kept must be contiguous int32 [batch, kv heads, keep]")
+    if new_lens.numel() != c.batch or new_lens.element_size() != 4:
+        raise ValueError("new_lens must be int32 [batch]")
+    ev = gtq_eviction(int(keep), int(n_first), int(n_recent))
+    ev.weights_dev, ev.w_strides = _ptr(weights), _weights2(weights, plan, "weights")
+    if weights_out is not None:
+        ev.weights_out_dev = _ptr(weights_out)
+        ev.w_out_strides = _weights2(weights_out, plan, "weights_out")
+    ev.kept_dev = _ptr(kept) or None
+    ev.new_lens_dev = _ptr(new_lens)
+    rc = _lib.gtq_evict(plan.handle, _ptr(packed), int(T), _lay(layout), ctypes.byref(ev),
+                        _ptr(dst), _nbytes(dst), _lay(dst_layout), _ptr(workspace),
+                        _nbytes(workspace), _stream(stream))
+    _check(rc, "gtq_evict")
 
 
 def gtq_free(plan: Plan) -> None:

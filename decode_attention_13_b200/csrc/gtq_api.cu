@@ -1,6 +1,7 @@
 // C ABI of libgtq: argument validation, plan lifetime and kernel launches.
 // Every entry point returns a GTQ_* code; nothing throws across the boundary.
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -120,6 +121,35 @@ int check_layout(const gtq_seq_layout* lay, int64_t T) {
     if ((T + kTile - 1) / kTile > lay->max_blocks) return GTQ_ERR_INVALID;
   }
   return GTQ_OK;
+}
+
+// The plan's device for the time of a call, whichever the caller has made current.
+struct OnDevice {
+  int prev = -1, want;
+  cudaError_t err;
+  explicit OnDevice(int device) : want(device) {
+    err = cudaGetDevice(&prev);
+    if (err == cudaSuccess && prev != want) err = cudaSetDevice(want);
+  }
+  ~OnDevice() {
+    if (prev >= 0 && prev != want) cudaSetDevice(prev);
+  }
+};
+
+// Arguments that the calls over several rows of a sequence share.
+int check_chunk(const gtq_plan* plan, const void* packed, int64_t T, const gtq_seq_layout* lay,
+                const gtq_chunk* c, const void* q, const void* workspace) {
+  if (!plan || !packed || !c || !q || !workspace) return GTQ_ERR_INVALID;
+  if (plan->cfg.head_dim != kD) return GTQ_ERR_UNSUPPORTED;
+  if (T < 1 || T > plan->cfg.t_capacity) return GTQ_ERR_INVALID;
+  if (c->n_tokens < 1 || c->n_tokens > (1 << 20) || c->reserved != 0) return GTQ_ERR_INVALID;
+  if (c->causal != 0 && c->causal != 1) return GTQ_ERR_INVALID;
+  if (c->chunk_lens_dev && !aligned(c->chunk_lens_dev, 4)) return GTQ_ERR_INVALID;
+  if (!aligned(packed, 16) || !aligned(q, 16) || !aligned(workspace, 256)) return GTQ_ERR_INVALID;
+  if (c->q_strides[3] != 1) return GTQ_ERR_INVALID;
+  for (int i = 0; i < 3; ++i)
+    if (c->q_strides[i] < 0 || c->q_strides[i] % 8) return GTQ_ERR_INVALID;
+  return check_layout(lay, T);
 }
 
 }  // namespace
@@ -282,6 +312,129 @@ int gtq_decode_attn_full(gtq_plan* plan, const void* packed_dev, int64_t T,
   if (check_layout(lay, T) != GTQ_OK) return GTQ_ERR_INVALID;
   return cuda_code(launch_decode(plan, (const uint8_t*)packed_dev, T, q_dev, q_dtype, out_dev,
                                  seq_map(plan, lay), f, (cudaStream_t)stream));
+}
+
+int gtq_rope(const gtq_rope_config* cfg, int64_t batch, int64_t tokens, const int64_t* positions_dev,
+             int64_t pos_stride, int64_t pos0, const gtq_rope_tensor* q, const gtq_rope_tensor* k,
+             void* stream) {
+  if (!cfg || (!q && !k)) return GTQ_ERR_INVALID;
+  const gtq_rope_config& c = *cfg;
+  if (c.head_dim < 2 || c.head_dim > 256 || (c.head_dim & 1)) return GTQ_ERR_INVALID;
+  if (c.rotary_dim < 2 || c.rotary_dim > c.head_dim || (c.rotary_dim & 1)) return GTQ_ERR_INVALID;
+  if (c.rope_pairing != GTQ_PAIRING_HALF && c.rope_pairing != GTQ_PAIRING_INTERLEAVED)
+    return GTQ_ERR_INVALID;
+  if (c.dtype != GTQ_DTYPE_FP16 && c.dtype != GTQ_DTYPE_FP32) return GTQ_ERR_INVALID;
+  if (c.scaling < GTQ_ROPE_PLAIN || c.scaling > GTQ_ROPE_YARN) return GTQ_ERR_INVALID;
+  if (c.backward != 0 && c.backward != 1) return GTQ_ERR_INVALID;
+  if (!(c.theta > 1.0) || !std::isfinite(c.theta) || !std::isfinite(c.magnitude))
+    return GTQ_ERR_INVALID;
+  if (c.scaling != GTQ_ROPE_PLAIN && !(c.factor >= 1.0 && std::isfinite(c.factor)))
+    return GTQ_ERR_INVALID;
+  if (c.scaling == GTQ_ROPE_LLAMA3 || c.scaling == GTQ_ROPE_YARN) {
+    if (!(c.original_context > 0.0) || !std::isfinite(c.original_context)) return GTQ_ERR_INVALID;
+    if (!(c.low_freq > 0.0) || !(c.high_freq > c.low_freq) || !std::isfinite(c.high_freq))
+      return GTQ_ERR_INVALID;
+  }
+  if (batch < 1 || tokens < 1 || pos_stride < 0) return GTQ_ERR_INVALID;
+  if (batch > 0x7fffffff || tokens > 0x7fffffff || batch * tokens > 0x7fffffff)
+    return GTQ_ERR_UNSUPPORTED;
+  if (positions_dev && !aligned(positions_dev, 8)) return GTQ_ERR_INVALID;
+  const size_t es = c.dtype == GTQ_DTYPE_FP16 ? 2 : 4;
+  for (const gtq_rope_tensor* t : {q, k}) {
+    if (!t) continue;
+    if (!t->x || !t->y || !aligned(t->x, es) || !aligned(t->y, es)) return GTQ_ERR_INVALID;
+    if (t->heads < 1 || t->heads > 65535 || t->reserved != 0) return GTQ_ERR_INVALID;
+    if (t->x_strides[3] != 1 || t->y_strides[3] != 1) return GTQ_ERR_INVALID;
+    for (int i = 0; i < 3; ++i)
+      if (t->x_strides[i] < 0 || t->y_strides[i] < 0) return GTQ_ERR_INVALID;
+  }
+  return cuda_code(launch_rope(c, batch, tokens, positions_dev, pos_stride, pos0, q, k,
+                               (cudaStream_t)stream));
+}
+
+size_t gtq_chunk_workspace_bytes(const gtq_plan* plan, int64_t T, int64_t n_tokens) {
+  if (!plan || T < 1 || T > plan->cfg.t_capacity || n_tokens < 1 || n_tokens > (1 << 20)) return 0;
+  return chunk_workspace(plan, T, n_tokens);
+}
+
+size_t gtq_weights_workspace_bytes(const gtq_plan* plan, int64_t T, int64_t n_tokens) {
+  if (!plan || T < 1 || T > plan->cfg.t_capacity || n_tokens < 1 || n_tokens > (1 << 20)) return 0;
+  return weights_workspace(plan, T, n_tokens);
+}
+
+size_t gtq_evict_workspace_bytes(const gtq_plan* plan, int64_t T) {
+  if (!plan || T < 1 || T > plan->cfg.t_capacity) return 0;
+  return (size_t)plan->n_heads * (size_t)T * sizeof(int32_t);
+}
+
+int gtq_chunk_attn(gtq_plan* plan, const void* packed_dev, int64_t T, const gtq_seq_layout* lay,
+                   const gtq_chunk* chunk, const void* q_dev, void* out_dev, void* workspace_dev,
+                   size_t workspace_bytes, void* stream) {
+  int rc = check_chunk(plan, packed_dev, T, lay, chunk, q_dev, workspace_dev);
+  if (rc != GTQ_OK) return rc;
+  if (plan->cfg.v_bits == 0) return GTQ_ERR_UNSUPPORTED;
+  if (!out_dev || !aligned(out_dev, 16) || chunk->out_strides[3] != 1) return GTQ_ERR_INVALID;
+  for (int i = 0; i < 3; ++i)
+    if (chunk->out_strides[i] < 0 || chunk->out_strides[i] % 8) return GTQ_ERR_INVALID;
+  if (workspace_bytes < chunk_workspace(plan, T, chunk->n_tokens)) return GTQ_ERR_INVALID;
+  OnDevice on(plan->device);
+  if (on.err != cudaSuccess) return cuda_code(on.err);
+  return cuda_code(launch_chunk(plan, (const uint8_t*)packed_dev, T, seq_map(plan, lay), *chunk,
+                                (const __half*)q_dev, (__half*)out_dev, (uint8_t*)workspace_dev,
+                                (cudaStream_t)stream));
+}
+
+int gtq_attn_weights(gtq_plan* plan, const void* packed_dev, int64_t T, const gtq_seq_layout* lay,
+                     const gtq_chunk* chunk, const void* q_dev, const float* weights_in_dev,
+                     float* weights_out_dev, const int64_t w_strides[2], void* workspace_dev,
+                     size_t workspace_bytes, void* stream) {
+  int rc = check_chunk(plan, packed_dev, T, lay, chunk, q_dev, workspace_dev);
+  if (rc != GTQ_OK) return rc;
+  if (!weights_out_dev || !w_strides || !aligned(weights_out_dev, 4) || !aligned(weights_in_dev, 4))
+    return GTQ_ERR_INVALID;
+  if (w_strides[0] < 0 || w_strides[1] < 0) return GTQ_ERR_INVALID;
+  if (workspace_bytes < weights_workspace(plan, T, chunk->n_tokens)) return GTQ_ERR_INVALID;
+  OnDevice on(plan->device);
+  if (on.err != cudaSuccess) return cuda_code(on.err);
+  return cuda_code(launch_weights(plan, (const uint8_t*)packed_dev, T, seq_map(plan, lay), *chunk,
+                                  (const __half*)q_dev, weights_in_dev, weights_out_dev, w_strides,
+                                  (uint8_t*)workspace_dev, (cudaStream_t)stream));
+}
+
+int gtq_evict(gtq_plan* plan, const void* src_dev, int64_t T, const gtq_seq_layout* lay,
+              const gtq_eviction* ev, void* dst_dev, size_t dst_bytes, const gtq_seq_layout* dst_lay,
+              void* workspace_dev, size_t workspace_bytes, void* stream) {
+  if (!plan || !src_dev || !ev || !dst_dev || !workspace_dev) return GTQ_ERR_INVALID;
+  if (plan->cfg.head_dim != kD) return GTQ_ERR_UNSUPPORTED;
+  if (T < 1 || T > plan->cfg.t_capacity) return GTQ_ERR_INVALID;
+  if (T > 0x7fffffff) return GTQ_ERR_UNSUPPORTED;  // indices are int32
+  if (ev->keep < 1 || ev->keep > plan->cfg.t_capacity || ev->n_first < 0 || ev->n_recent < 0)
+    return GTQ_ERR_INVALID;
+  if (ev->n_first > ev->keep || ev->n_recent > ev->keep - ev->n_first) return GTQ_ERR_INVALID;
+  if (!ev->weights_dev || !ev->new_lens_dev || !aligned(ev->weights_dev, 4) ||
+      !aligned(ev->weights_out_dev, 4) || !aligned(ev->kept_dev, 4) || !aligned(ev->new_lens_dev, 4))
+    return GTQ_ERR_INVALID;
+  for (int i = 0; i < 2; ++i)
+    if (ev->w_strides[i] < 0 || (ev->weights_out_dev && ev->w_out_strides[i] < 0))
+      return GTQ_ERR_INVALID;
+  if (!aligned(src_dev, 16) || !aligned(dst_dev, 16) || !aligned(workspace_dev, 256))
+    return GTQ_ERR_INVALID;
+  if (check_layout(lay, T) != GTQ_OK ||
+      check_layout(dst_lay, std::min(ev->keep, T)) != GTQ_OK)
+    return GTQ_ERR_INVALID;
+  const bool paged = lay && lay->block_table_dev, dst_paged = dst_lay && dst_lay->block_table_dev;
+  const size_t need = dst_paged ? (size_t)plan->cfg.n_kv_heads * plan->tile_bytes : plan->packed_bytes;
+  if (dst_bytes < need) return GTQ_ERR_INVALID;
+  if (!paged && !dst_paged) {  // two contiguous caches: their ranges are known here
+    const uintptr_t s = (uintptr_t)src_dev, d = (uintptr_t)dst_dev;
+    if (s < d + plan->packed_bytes && d < s + plan->packed_bytes) return GTQ_ERR_INVALID;
+  }
+  if (workspace_bytes < gtq_evict_workspace_bytes(plan, T)) return GTQ_ERR_INVALID;
+  OnDevice on(plan->device);
+  if (on.err != cudaSuccess) return cuda_code(on.err);
+  return cuda_code(launch_evict(plan, (const uint8_t*)src_dev, T, seq_map(plan, lay), *ev,
+                                (uint8_t*)dst_dev, seq_map(plan, dst_lay), (int32_t*)workspace_dev,
+                                (cudaStream_t)stream));
 }
 
 int gtq_free(gtq_plan* plan) {

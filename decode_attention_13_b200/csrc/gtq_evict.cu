@@ -1,0 +1,449 @@
+// Eviction (include/gtq.h, gtq_evict): of every (sequence, KV head) the first
+// and last tokens and those with the largest weights stay, and their codes move
+// to another packed cache.  Two launches.
+//
+// select_kernel: one cluster of up to 8 blocks per head.  The weight that the
+// last chosen token has is found digit by digit (11, 11 and 10 bits of the
+// weight's order-preserving integer): each block counts the digits of its own
+// stretch of tokens, the cluster adds the counts through distributed shared
+// memory, and every block finds the digit where the count from the top passes
+// what is still wanted.  A last pass writes the indices in order: tokens above
+// that weight, and as many with exactly that weight, lowest index first, as are
+// missing.  It reads the weights four times (once from HBM, then from L2) and is
+// bound by the latency of its passes.
+//
+// move_kernel: one block per new tile and head.  The tiles that its 64 tokens
+// come from arrive by bulk copy, kBatch at a time; a thread owns portions of the
+// new tile (all codes of 8 or 16 of its tokens in one slot or pair of dims), puts
+// them together in registers from two-word reads of the old tiles, and adds them
+// to the tile in shared memory, which leaves in full.  Bound by the bytes of the
+// source tiles (HBM reads them in sectors that hold the codes of many tokens) and
+// by the instructions of taking codes apart.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "gtq_internal.h"
+
+namespace cg = cooperative_groups;
+
+namespace gtq {
+namespace {
+
+constexpr int kSelThreads = 1024;
+constexpr int kSelBins = 2048;
+constexpr int kSelCluster = 8;       // blocks per head at most (portable cluster size)
+constexpr int kSelTokens = 4096;     // tokens that are worth a block of their own
+constexpr int kMoveThreads = 256;
+constexpr int kBatch = 8;            // source tiles in shared memory at once
+
+struct EvictArgs {
+  const float* w;
+  int64_t ws[2];
+  float* w_out;
+  int64_t wos[2];
+  int32_t* kept;        // [heads][kept_stride]
+  int64_t kept_stride;
+  int64_t fill;         // entries of kept that are written (behind the last: -1)
+  int32_t* new_lens;
+  int64_t T, keep, first, recent;
+  int hkv;
+  SeqMap src, dst;
+  const uint8_t* src_packed;
+  uint8_t* dst_packed;
+  const HeadMeta* meta;
+  int kb, vb;
+};
+
+// Larger weight, larger integer; -0 as +0, NaN below everything.
+__device__ __forceinline__ uint32_t order_key(float w) {
+  if (w != w) return 0u;
+  const uint32_t u = __float_as_uint(w + 0.f);
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+// Exclusive prefix sum of one int per thread over the block; `total` for all.
+__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int s = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    warp_sums[lane] = s;
+  }
+  __syncthreads();
+  total = warp_sums[31];
+  const int before = warp ? warp_sums[warp - 1] : 0;
+  __syncthreads();
+  return before + x - v;
+}
+
+__global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a) {
+  __shared__ int hist[kSelBins];
+  __shared__ int warp_sums[32];
+  __shared__ int found[2];   // digit, and the count above it
+  __shared__ int counts[2];  // this block's tokens that are sure to stay, and those at the weight
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank(), blocks = (int)cluster.num_blocks();
+  const int head = blockIdx.y, b = head / a.hkv, h = head % a.hkv;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int64_t len = a.src.len(b, a.T);
+  const int64_t n_keep = len < a.keep ? len : a.keep;
+  const int64_t first = a.first < len ? a.first : len;
+  const int64_t last = len - a.recent > first ? len - a.recent : first;  // [first, last) compete
+  int64_t want = n_keep - (first + len - last);
+  const float* w = a.w + b * a.ws[0] + h * a.ws[1];
+  // this block's stretch, a multiple of the block's threads
+  const int64_t part = (len + blocks - 1) / blocks;
+  const int64_t per = (part + kSelThreads - 1) / kSelThreads * kSelThreads;
+  const int64_t t0 = per * rank < len ? per * rank : len, t1 = t0 + per < len ? t0 + per : len;
+  const bool all = n_keep == len;  // nothing is left out (uniform over the cluster)
+  uint32_t prefix = 0;
+  if (!all) {
+    int shift = 32;
+    for (int pass = 0; pass < 3; ++pass) {
+      const int bits = pass < 2 ? 11 : 10;
+      const uint32_t above = pass == 0 ? 0u : ~0u << shift;
+      shift -= bits;
+      for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
+      __syncthreads();
+      for (int64_t base = t0; base < t1; base += kSelThreads) {
+        const int64_t t = base + tid;
+        bool on = t < t1 && t >= first && t < last;
+        int bin = -1;
+        if (on) {
+          const uint32_t k = order_key(w[t]);
+          on = (k & above) == prefix;
+          bin = on ? (int)((k >> shift) & ((1u << bits) - 1)) : -1;
+        }
+        // equal digits are common (weights of 0, near-equal exponents): the lanes that
+        // agree with the first one count once
+        const unsigned live = __ballot_sync(0xffffffffu, on);
+        if (live) {
+          const int lead = __ffs(live) - 1;
+          const int same = __shfl_sync(0xffffffffu, bin, lead);
+          const unsigned agree = __ballot_sync(0xffffffffu, on && bin == same);
+          if (lane == lead) atomicAdd(&hist[same], __popc(agree));
+          else if (on && bin != same) atomicAdd(&hist[bin], 1);
+        }
+      }
+      cluster.sync();
+      // bins from the top, two per thread: digit d = bins - 1 - i
+      const int n_bins = 1 << bits;
+      int c[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int d = n_bins - 1 - (2 * tid + e);
+        c[e] = 0;
+        if (d >= 0)
+          for (int r = 0; r < blocks; ++r) c[e] += *cluster.map_shared_rank(&hist[d], r);
+      }
+      int total;
+      const int before = block_scan(c[0] + c[1], warp_sums, total);
+      const int wanted = (int)want;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int over = before + (e ? c[0] : 0);
+        if (over < wanted && over + c[e] >= wanted) {
+          found[0] = n_bins - 1 - (2 * tid + e);
+          found[1] = over;
+        }
+      }
+      // no block clears its counts while another still reads them
+      cluster.sync();
+      if (wanted > 0) {
+        prefix |= (uint32_t)found[0] << shift;
+        want -= found[1];
+      } else {  // only the first and last tokens stay: nothing is above the largest integer
+        prefix = ~0u;
+      }
+      __syncthreads();
+    }
+    if (want <= 0) want = 0;
+  }
+  // want: how many of the tokens whose integer is `prefix` stay
+  auto klass = [&](int64_t t) {  // 2 stays, 1 at the weight, 0 goes
+    if (t >= t1) return 0;
+    if (all || t < first || t >= last) return 2;
+    const uint32_t k = order_key(w[t]);
+    return k > prefix ? 2 : (k == prefix && want > 0 ? 1 : 0);
+  };
+  if (tid < 2) counts[tid] = 0;
+  __syncthreads();
+  int sure = 0, equal = 0;
+  for (int64_t t = t0 + tid; t < t1; t += kSelThreads) {
+    const int c = klass(t);
+    sure += c == 2;
+    equal += c == 1;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    sure += __shfl_xor_sync(0xffffffffu, sure, o);
+    equal += __shfl_xor_sync(0xffffffffu, equal, o);
+  }
+  if (lane == 0) {
+    atomicAdd(&counts[0], sure);
+    atomicAdd(&counts[1], equal);
+  }
+  cluster.sync();
+  int64_t out = 0, eq = 0;  // tokens kept, and tokens at the weight, before this block's
+  for (int r = 0; r < rank; ++r) {
+    out += *cluster.map_shared_rank(&counts[0], r);
+    eq += *cluster.map_shared_rank(&counts[1], r);
+  }
+  cluster.sync();  // nothing of another block is read past this point
+  out += eq < want ? eq : want;
+  int32_t* kept = a.kept + (int64_t)head * a.kept_stride;
+  float* wo = a.w_out ? a.w_out + b * a.wos[0] + h * a.wos[1] : nullptr;
+  for (int64_t base = t0; base < t1; base += kSelThreads) {
+    const int64_t t = base + tid;
+    const int c = klass(t);
+    int n_eq, n_out;
+    const int eq_here = block_scan(c == 1, warp_sums, n_eq);
+    const bool stays = c == 2 || (c == 1 && eq + eq_here < want);
+    const int at = block_scan(stays, warp_sums, n_out);
+    if (stays) {
+      kept[out + at] = (int32_t)t;
+      if (wo) wo[out + at] = w[t];
+    }
+    eq += n_eq;
+    out += n_out;
+  }
+  for (int64_t i = n_keep + (int64_t)rank * kSelThreads + tid; i < a.fill; i += (int64_t)blocks * kSelThreads)
+    kept[i] = -1;
+  if (h == 0 && rank == 0 && tid == 0) a.new_lens[b] = (int32_t)n_keep;
+}
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+
+// 32 bits from bit `at` of a word array
+__device__ __forceinline__ uint32_t bits_at(const uint32_t* x, int at) {
+  const int i = at >> 5;
+  return __funnelshift_r(x[i], x[i + 1], at & 31);
+}
+
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(EvictArgs a, int* status) {
+  extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ HeadMeta m;
+  __shared__ int src_tile[kTile];    // distinct source tiles, in order
+  __shared__ uint8_t slot_of[kTile]; // token -> its place in that list
+  __shared__ uint8_t tok_in[kTile];  // token -> its index in its source tile
+  __shared__ int n_src;
+  __shared__ __align__(8) uint64_t bar;
+  const int head = blockIdx.y, b = head / a.hkv;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int64_t len = a.src.len(b, a.T);
+  const int64_t n_keep = len < a.keep ? len : a.keep;
+  const int64_t tile = blockIdx.x;
+  if (tile * kTile >= n_keep) return;
+  const int n_tok = (int)(n_keep - tile * kTile < kTile ? n_keep - tile * kTile : kTile);
+  const int tb = (int)a.src.tile_bytes;
+  uint32_t* out = reinterpret_cast<uint32_t*>(sm);
+  const uint32_t stage = (uint32_t)tb + 16;  // a word behind each tile may be read
+  for (int i = tid; i < tb / 16; i += kMoveThreads) reinterpret_cast<uint4*>(sm)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = tid; i < (int)(sizeof(HeadMeta) / 4); i += kMoveThreads)
+    reinterpret_cast<uint32_t*>(&m)[i] = reinterpret_cast<const uint32_t*>(a.meta + head)[i];
+  if (tid < 32) {  // which tiles the tokens come from: they are in order
+    const int32_t* kept = a.kept + (int64_t)head * a.kept_stride + tile * kTile;
+    int before = 0;
+    int prev_last = -1;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int i = 32 * half + lane;
+      const int s = i < n_tok ? kept[i] : -1;
+      const int st = s >> 6;
+      int up = __shfl_up_sync(0xffffffffu, st, 1);
+      if (lane == 0) up = prev_last;
+      const bool fresh = s >= 0 && st != up;
+      const unsigned f = __ballot_sync(0xffffffffu, fresh);
+      const int at = before + __popc(f & ((2u << lane) - 1)) - 1;
+      if (s >= 0) {
+        slot_of[i] = (uint8_t)at;
+        tok_in[i] = (uint8_t)(s & 63);
+        if (fresh) src_tile[at] = st;
+      }
+      before += __popc(f);
+      prev_last = __shfl_sync(0xffffffffu, st, 31);
+    }
+    if (lane == 0) {
+      n_src = before;
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&bar)));
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+  }
+  __syncthreads();
+  const int kb = a.kb, vb = a.vb;
+  bool ok = true;
+  for (int s0 = 0, round = 0; s0 < n_src && ok; s0 += kBatch, ++round) {
+    const int n = min(kBatch, n_src - s0);
+    if (tid == 0) {
+      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(&bar)),
+                   "r"((uint32_t)(n * tb)) : "memory");
+      for (int i = 0; i < n; ++i)
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                smem_addr(sm + tb + i * stage)),
+            "l"(a.src.tile(const_cast<uint8_t*>(a.src_packed), head, src_tile[s0 + i])), "r"((uint32_t)tb),
+            "r"(smem_addr(&bar))
+            : "memory");
+    }
+    {  // bounded wait: after 2 s the call has failed, after 2 s more its copies are given up
+      uint64_t began = 0;
+      for (unsigned i = 0;; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(done) : "r"(smem_addr(&bar)), "r"(round & 1), "r"(1000000u) : "memory");
+        if (done) break;
+        uint64_t now;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+        if (!began) began = now;
+        else if (now - began > 4000000000ull) break;
+        else if (now - began > 2000000000ull) ok = false;
+      }
+    }
+    if (__syncthreads_or(!ok)) { ok = false; break; }
+    auto source = [&](int j) -> const uint32_t* {  // token j's old tile, or null if not in this batch
+      const int i = (int)slot_of[j] - s0;
+      return j < n_tok && i >= 0 && i < n ? reinterpret_cast<const uint32_t*>(sm + tb + i * stage) : nullptr;
+    };
+    // keys: portion g of slot s holds the pairs of tokens g + 8 u, 2 w bits each
+    for (int i = tid; i < m.n_slots * 8; i += kMoveThreads) {
+      const int s = i >> 3, g = i & 7, w = m.slot_width[s], w2 = 2 * w;
+      const int area = 8 * m.slot_koff[s];
+      uint32_t acc[4] = {0, 0, 0, 0};
+      for (int u = 0; u < 8; ++u) {
+        const uint32_t* x = source(g + 8 * u);
+        if (!x) continue;
+        const int js = tok_in[g + 8 * u];
+        const uint32_t pair = bits_at(x, area + (js & 7) * 16 * w + (js >> 3) * w2) & ((1u << w2) - 1);
+        const int at = u * w2, q = at >> 5, sh = at & 31;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (k == q) acc[k] |= pair << sh;
+          if (k == q + 1 && sh) acc[k] |= pair >> (32 - sh);
+        }
+      }
+      // 16 w bits at a multiple of 16 bits
+      uint16_t* o = reinterpret_cast<uint16_t*>(sm) + (area >> 4) + g * w;
+      for (int k = 0; k < w; ++k) o[k] |= (uint16_t)(acc[k >> 1] >> (16 * (k & 1)));
+    }
+    // values: portion (i8, g, c) holds dims 16 i8 + g, + 8 of 16 tokens, 32 codes
+    if (vb) {
+      const uint32_t mask = (1u << vb) - 1;
+      for (int p = tid; p < 256; p += kMoveThreads) {
+        const int c = p & 3, ig = p >> 2;
+        uint32_t acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int k = 0; k < 16; ++k) {
+          const int j = 16 * (k >> 2) + 8 * ((k >> 1) & 1) + 2 * c + (k & 1);
+          const uint32_t* x = source(j);
+          if (!x) continue;
+          const int js = tok_in[j];
+          const int xs = 8 * (js >> 4) + 4 * ((js >> 3) & 1) + (js & 1);
+          const uint32_t v = bits_at(x, 8192 * kb + (ig * 4 + ((js & 7) >> 1)) * 32 * vb + xs * vb);
+          const int xd = 8 * (k >> 2) + 4 * ((k >> 1) & 1) + (k & 1);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t code = (v >> (2 * e * vb)) & mask;
+            const int at = (xd + 2 * e) * vb, q = at >> 5, sh = at & 31;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+              if (r == q) acc[r] |= code << sh;
+              if (r == q + 1 && sh) acc[r] |= code >> (32 - sh);
+            }
+          }
+        }
+        uint32_t* o = out + 256 * kb + p * vb;
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r < vb) o[r] |= acc[r];
+      }
+    }
+    // norms: row of 64 fp16, token j at (j & 7) * 8 + (j >> 3); the value norms, then the groups'
+    const int n_rows = (vb ? 1 : 0) + m.n_groups;
+    for (int i = tid; i < n_rows * kTile; i += kMoveThreads) {
+      const int row = i >> 6, j = i & 63;
+      const uint32_t* x = source(j);
+      if (!x) continue;
+      const int js = tok_in[j];
+      const int o = 512 * (kb + vb) + row * 64;
+      reinterpret_cast<uint16_t*>(sm)[o + (j & 7) * 8 + (j >> 3)] =
+          reinterpret_cast<const uint16_t*>(x)[o + (js & 7) * 8 + (js >> 3)];
+    }
+    __syncthreads();  // the batch is read before the next one lands on it
+  }
+  if (!ok) {
+    if (tid == 0) atomicOr(status, kStatusTimeout);
+    return;
+  }
+  uint4* dst = reinterpret_cast<uint4*>(a.dst.tile(a.dst_packed, head, tile));
+  for (int i = tid; i < tb / 16; i += kMoveThreads) dst[i] = reinterpret_cast<const uint4*>(sm)[i];
+}
+
+}  // namespace
+
+cudaError_t launch_evict(const gtq_plan* p, const uint8_t* src, int64_t T, const SeqMap& sm,
+                         const gtq_eviction& ev, uint8_t* dst, const SeqMap& dm, int32_t* ws_kept,
+                         cudaStream_t s) {
+  EvictArgs a;
+  a.w = ev.weights_dev;
+  a.w_out = ev.weights_out_dev;
+  for (int i = 0; i < 2; ++i) {
+    a.ws[i] = ev.w_strides[i];
+    a.wos[i] = ev.w_out_strides[i];
+  }
+  a.kept = ev.kept_dev ? ev.kept_dev : ws_kept;
+  a.kept_stride = ev.kept_dev ? ev.keep : T;
+  a.fill = ev.kept_dev ? ev.keep : 0;
+  a.new_lens = ev.new_lens_dev;
+  a.T = T;
+  a.keep = ev.keep;
+  a.first = ev.n_first;
+  a.recent = ev.n_recent;
+  a.hkv = p->cfg.n_kv_heads;
+  a.src = sm;
+  a.dst = dm;
+  a.src_packed = src;
+  a.dst_packed = dst;
+  a.meta = p->d_meta;
+  a.kb = p->cfg.k_bits;
+  a.vb = p->cfg.v_bits;
+  int blocks = 1;
+  while (blocks < kSelCluster && T > (int64_t)blocks * kSelTokens) blocks *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks, (unsigned)p->n_heads);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)blocks;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, select_kernel, a);
+  if (e != cudaSuccess) return e;
+  const int64_t most = std::min(ev.keep, T);
+  const size_t smem = p->tile_bytes + kBatch * (p->tile_bytes + 16);
+  e = cudaFuncSetAttribute(move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  move_kernel<<<dim3((unsigned)((most + kTile - 1) / kTile), (unsigned)p->n_heads), kMoveThreads, smem, s>>>(
+      a, p->d_status);
+  return cudaGetLastError();
+}
+
+}  // namespace gtq

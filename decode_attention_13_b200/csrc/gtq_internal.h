@@ -281,4 +281,22 @@ struct Fp16Kv {
 cudaError_t launch_decode(const gtq_plan* p, const uint8_t* packed, int64_t T, const void* q,
                           int q_dtype, float* out, const SeqMap& sm, const Fp16Kv& kv,
                           cudaStream_t s);
+
+// Rotary positions (gtq_rope.cu); q or k may be null
+cudaError_t launch_rope(const gtq_rope_config& c, int64_t batch, int64_t tokens, const int64_t* pos,
+                        int64_t pos_stride, int64_t pos0, const gtq_rope_tensor* q,
+                        const gtq_rope_tensor* k, cudaStream_t s);
+// Attention of a chunk and the weights it gives
+size_t chunk_workspace(const gtq_plan* p, int64_t T, int64_t n);
+cudaError_t launch_chunk(const gtq_plan* p, const uint8_t* packed, int64_t T, const SeqMap& sm,
+                         const gtq_chunk& c, const __half* q, __half* out, uint8_t* workspace,
+                         cudaStream_t s);
+size_t weights_workspace(const gtq_plan* p, int64_t T, int64_t n);
+cudaError_t launch_weights(const gtq_plan* p, const uint8_t* packed, int64_t T, const SeqMap& sm,
+                           const gtq_chunk& c, const __half* q, const float* w_in, float* w_out,
+                           const int64_t* w_strides, uint8_t* workspace, cudaStream_t s);
+// Eviction (gtq_evict.cu); ws_kept: int32 [heads][T], used when ev.kept_dev is null
+cudaError_t launch_evict(const gtq_plan* p, const uint8_t* src, int64_t T, const SeqMap& sm,
+                         const gtq_eviction& ev, uint8_t* dst, const SeqMap& dm, int32_t* ws_kept,
+                         cudaStream_t s);
 }  // namespace gtq

@@ -13,6 +13,11 @@
  *                      into the packed cache
  *   gtq_decode_attn    fused GQA decode attention read directly from the codes
  *   gtq_free           release a plan
+ * and the operators around it that serving needs:
+ *   gtq_rope           rotary positions of queries and keys
+ *   gtq_chunk_attn     attention of several new tokens per sequence over the cache
+ *   gtq_attn_weights   the attention weight each cached token got
+ *   gtq_evict          the tokens with the largest weights, moved to a new cache
  *
  * Construction (the page gives the ideas, not formulas; these are the readings
  * this library implements):
@@ -274,6 +279,193 @@ GTQ_API int gtq_decode_attn_full(gtq_plan* plan, const void* packed_dev, int64_t
                                  const gtq_seq_layout* lay, const gtq_fp16_kv* kv,
                                  const void* q_dev, int32_t q_dtype, float* out_dev,
                                  void* stream);
+
+/* ---- rotary positions ---------------------------------------------------- */
+
+#define GTQ_ROPE_PLAIN 0  /* f_i = theta^(-2 i / rotary_dim)                          */
+#define GTQ_ROPE_LINEAR 1 /* every f_i divided by factor                              */
+#define GTQ_ROPE_LLAMA3 2 /* slow pairs divided by factor, ramp over turns            */
+#define GTQ_ROPE_YARN 3   /* slow pairs divided by factor, ramp over the pair's index */
+
+/*
+ * Rotary positions (RoPE) of one layer: the keys that gtq_alloc_bits and
+ * gtq_quantize_pack take, and the queries of every attention call, are
+ * post-RoPE.  Pair i (0 <= i < rotary_dim / 2) of a row at position p turns by
+ * the angle a = p f_i:
+ *     y0 = magnitude (x0 cos a - x1 sin a),  y1 = magnitude (x1 cos a + x0 sin a)
+ * HALF pairs dims (i, i + rotary_dim / 2), INTERLEAVED (2i, 2i + 1); dims from
+ * rotary_dim on are copied.  Angles are formed in fp64 and reduced to one turn
+ * before their sine and cosine (exact to 2^-23 at any position below 2^53).
+ * Scaling for contexts longer than original_context: with n_i = original_context
+ * f_i / (2 pi) the turns a pair makes over it,
+ *     LLAMA3  s = clamp((n_i - low_freq) / (high_freq - low_freq), 0, 1),
+ *             f_i <- (1 - s) f_i / factor + s f_i
+ *     YARN    with c(n) = rotary_dim ln(original_context / (2 pi n)) / (2 ln theta),
+ *             lo = max(floor(c(high_freq)), 0), hi = min(ceil(c(low_freq)), rotary_dim - 1),
+ *             s = clamp((i - lo) / max(hi - lo, 0.001), 0, 1),
+ *             f_i <- s f_i / factor + (1 - s) f_i
+ * backward = 1 turns by -a: the transposed matrix, i.e. the gradient with respect
+ * to x of an output gradient (and, at magnitude 1, the inverse).
+ */
+typedef struct gtq_rope_config {
+  int32_t head_dim;     /* even, 2..256                                          */
+  int32_t rotary_dim;   /* even, 2..head_dim                                     */
+  int32_t rope_pairing; /* GTQ_PAIRING_*                                         */
+  int32_t dtype;        /* GTQ_DTYPE_* of x and y                                */
+  int32_t scaling;      /* GTQ_ROPE_*                                            */
+  int32_t backward;     /* 0 or 1                                                */
+  double theta;         /* > 1                                                   */
+  double factor;        /* >= 1 (LINEAR, LLAMA3, YARN)                           */
+  double original_context; /* > 0 (LLAMA3, YARN)                                 */
+  double low_freq;      /* turns, 0 < low_freq < high_freq (LLAMA3, YARN)        */
+  double high_freq;
+  double magnitude;     /* finite; 1 leaves lengths alone                        */
+} gtq_rope_config;
+
+/* One tensor of rows: x element (b, h, t, i) at x + b*x_strides[0] +
+ * h*x_strides[1] + t*x_strides[2] + i (strides in elements, x_strides[3] must be
+ * 1, none negative), y likewise.  y may be x with the same strides (in place);
+ * any other overlap is not supported.  No alignment beyond the element's own. */
+typedef struct gtq_rope_tensor {
+  const void* x;
+  void* y;
+  int32_t heads;
+  int32_t reserved; /* must be 0 */
+  int64_t x_strides[4];
+  int64_t y_strides[4];
+} gtq_rope_tensor;
+
+/*
+ * gtq_rope -- rotate the queries and / or keys of batch x tokens positions.
+ *   positions_dev  int64, position of token t of sequence b at
+ *                  positions_dev[b * pos_stride + t] (pos_stride 0: one row for
+ *                  all), or NULL: pos0 + t.  Read in stream order.
+ *   q, k           tensors of n heads each; either may be NULL, not both.  One
+ *                  launch serves both, and the angles are formed once.
+ * Runs on the current device, which must be the tensors'.
+ * Errors: INVALID, UNSUPPORTED (batch * tokens above 2^31 - 1), CUDA.
+ */
+GTQ_API int gtq_rope(const gtq_rope_config* cfg, int64_t batch, int64_t tokens,
+                     const int64_t* positions_dev, int64_t pos_stride, int64_t pos0,
+                     const gtq_rope_tensor* q, const gtq_rope_tensor* k, void* stream);
+
+/* ---- several new tokens per sequence -------------------------------------- */
+
+/*
+ * A chunk: the last rows of every sequence as queries.  Sequence b brings n_b
+ * of them (chunk_lens_dev[b] clamped to [0, n_tokens], or n_tokens), whose own
+ * keys and values are in the cache already (gtq_quantize_pack_ex with
+ * GTQ_T0_TAIL appends them): row i of sequence b stands at position
+ * len_b - n_b + i.
+ *   causal = 1: row i sees the tokens at positions <= its own; a row that stands
+ *               before the cache's first token sees none.
+ *   causal = 0: every row sees all len_b tokens.
+ *   q_strides   strides of q in elements, element (b, hq, i, dim) at q + b*s[0] +
+ *               hq*s[1] + i*s[2] + dim (s[3] must be 1, the others multiples of
+ *               8 and not negative; q 16-byte aligned).
+ *   out_strides the same for out (gtq_chunk_attn); rows must not overlap.
+ */
+typedef struct gtq_chunk {
+  int64_t n_tokens;              /* rows per sequence at most, 1..2^20 */
+  const int32_t* chunk_lens_dev; /* device int32 [batch], or NULL      */
+  int32_t causal;
+  int32_t reserved;              /* must be 0 */
+  int64_t q_strides[4];
+  int64_t out_strides[4];
+} gtq_chunk;
+
+/*
+ * gtq_chunk_attn -- GQA attention of a chunk over the packed cache, by the
+ * formulas of gtq_decode_attn: a following turn of a conversation, drafted
+ * tokens to be verified, a long prompt taken in piece by piece, or (n_tokens 1)
+ * one decode step.
+ *   packed_dev, T, lay  as gtq_decode_attn_ex (contiguous or paged; lengths).
+ *   q_dev     fp16 post-RoPE queries; query head hq uses KV head hq / (Hq / Hkv).
+ *   out_dev   fp16, 16-byte aligned.  Rows i >= n_b are left as they are; a row
+ *             that sees no token gets zeros.
+ *   workspace_dev  workspace_bytes >= gtq_chunk_workspace_bytes(plan, T, n_tokens),
+ *             256-byte aligned.  It holds nothing between calls; calls that may
+ *             overlap (other streams, graphs replayed at once) need one each.
+ * Keys are attended with the wide groups' products in split fp16 and the others
+ * in fp16, as in gtq_decode_attn; scores, softmax statistics and sums are fp32.
+ * Errors: INVALID, UNSUPPORTED (head_dim != 128; a K-only plan), CUDA.
+ */
+GTQ_API int gtq_chunk_attn(gtq_plan* plan, const void* packed_dev, int64_t T,
+                           const gtq_seq_layout* lay, const gtq_chunk* chunk, const void* q_dev,
+                           void* out_dev, void* workspace_dev, size_t workspace_bytes,
+                           void* stream);
+GTQ_API size_t gtq_chunk_workspace_bytes(const gtq_plan* plan, int64_t T, int64_t n_tokens);
+
+/*
+ * gtq_attn_weights -- the attention weight every cached token got from a chunk,
+ * added up: for t < len_b
+ *     out[b][h][t] = in[b][h][t] + sum over the n_b rows and the query heads of
+ *                    KV head h of softmax(row)[t]
+ * (a row that sees no token adds nothing).  It is what gtq_evict chooses by.
+ *   weights_in_dev   fp32, element (b, h, t) at b*w_strides[0] + h*w_strides[1] + t,
+ *                    or NULL: zeros.  May be weights_out_dev.
+ *   weights_out_dev  fp32, the same strides (not negative); elements t >= len_b are
+ *                    left as they are.
+ *   others           as gtq_chunk_attn (out_strides are not read);
+ *                    workspace_bytes >= gtq_weights_workspace_bytes(...).
+ * Sums run in a fixed order: the same call gives the same bits.  Scores are
+ * exact to about 2^-21 of the largest product.  K-only plans are supported.
+ * Errors: INVALID, UNSUPPORTED (head_dim != 128), CUDA.
+ */
+GTQ_API int gtq_attn_weights(gtq_plan* plan, const void* packed_dev, int64_t T,
+                             const gtq_seq_layout* lay, const gtq_chunk* chunk, const void* q_dev,
+                             const float* weights_in_dev, float* weights_out_dev,
+                             const int64_t w_strides[2], void* workspace_dev,
+                             size_t workspace_bytes, void* stream);
+GTQ_API size_t gtq_weights_workspace_bytes(const gtq_plan* plan, int64_t T, int64_t n_tokens);
+
+/* ---- a cache held at a size ------------------------------------------------ */
+
+/*
+ * What gtq_evict keeps of every (sequence, KV head): sequence b goes from len_b
+ * to min(len_b, keep) tokens.  The first n_first and the last n_recent tokens
+ * stay; the others that stay are those with the largest weights (ties, and -0
+ * against +0, to the lower index; NaN counts as the least).  Tokens keep their
+ * order; keys keep the positions they were rotated to.
+ */
+typedef struct gtq_eviction {
+  int64_t keep;                /* 1..t_capacity                                 */
+  int64_t n_first;             /* >= 0, n_first + n_recent <= keep              */
+  int64_t n_recent;            /* >= 0                                          */
+  const float* weights_dev;    /* element (b, h, t) at b*s[0] + h*s[1] + t      */
+  int64_t w_strides[2];        /* s, not negative                               */
+  float* weights_out_dev;      /* weights of the kept tokens, or NULL           */
+  int64_t w_out_strides[2];    /* element (b, h, r) at b*s[0] + h*s[1] + r      */
+  int32_t* kept_dev;           /* int32 [batch][n_kv_heads][keep]: old index of */
+                               /* each kept token, -1 behind the last; or NULL  */
+  int32_t* new_lens_dev;       /* int32 [batch]: min(len_b, keep)               */
+} gtq_eviction;
+
+/*
+ * gtq_evict -- move the tokens that stay into another cache of the same plan.
+ *   src_dev, T, lay  the cache as gtq_decode_attn_ex reads it.
+ *   dst_dev          the new cache, 16-byte aligned, dst_bytes as packed_bytes of
+ *                    gtq_quantize_pack_ex; tiles below ceil(min(len_b, keep) / 64)
+ *                    are written in full (bits of tokens behind the last, and norms
+ *                    of groups a head does not have, are 0), others not at all.
+ *   dst_lay          NULL (contiguous) or a layout whose block table names the new
+ *                    pages (its lengths are not read; max_blocks * 64 >= keep).
+ *                    dst must not overlap the source tiles: a contiguous dst_dev
+ *                    inside a contiguous src is refused, pages are the caller's
+ *                    (new pages of the same pool are fine).
+ *   weights_out_dev, kept_dev  must not overlap the inputs; elements of
+ *                    weights_out behind the last kept token are left as they are.
+ *   workspace_dev    workspace_bytes >= gtq_evict_workspace_bytes(plan, T), 256-byte
+ *                    aligned, one per call that may overlap.
+ * The plan's allocation stays; appends, decodes and chunks go on over the new
+ * cache with new_lens_dev as its lengths.
+ * Errors: INVALID, UNSUPPORTED (head_dim != 128), CUDA.
+ */
+GTQ_API int gtq_evict(gtq_plan* plan, const void* src_dev, int64_t T, const gtq_seq_layout* lay,
+                      const gtq_eviction* ev, void* dst_dev, size_t dst_bytes,
+                      const gtq_seq_layout* dst_lay, void* workspace_dev, size_t workspace_bytes,
+                      void* stream);
+GTQ_API size_t gtq_evict_workspace_bytes(const gtq_plan* plan, int64_t T);
 
 /* gtq_free -- release the plan and its device memory.  Synchronises the plan's
  * device (cudaFree).  NULL is accepted.  Returns GTQ_OK or GTQ_ERR_CUDA. */
