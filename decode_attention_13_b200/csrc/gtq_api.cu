@@ -507,7 +507,7 @@ int gtq_status(gtq_plan* plan) {
   if (e == cudaSuccess) e = cudaMemset(plan->d_status, 0, sizeof(int));
   if (e != cudaSuccess) return GTQ_ERR_CUDA;
   if (v & kStatusLayout) {
-    set_last_error("decode kernel: shared-memory window above the planned layout");
+    set_last_error("a kernel's shared-memory window does not fit its planned layout");
     return GTQ_ERR_CUDA;
   }
   if (v & kStatusTimeout) return GTQ_ERR_TIMEOUT;

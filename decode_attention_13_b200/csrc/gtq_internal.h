@@ -193,6 +193,7 @@ struct Tables {
   float* thr;        // fp32 thresholds, width w at thr_base(w)
   uint4* dec_image;  // kDecodeImageBytes: the decode kernel's lookup tables
   uint8_t* rv_image; // R_V as the quantizer's tensor-core B operand (fp16 hi + lo, 64 KB)
+  uint8_t* rvt_image; // R_V^T likewise: outputs back from the values' basis
   uint8_t* code_lut; // kCodeLutBytes: CodeLutMeta + cells (built on the device from thr)
 };
 

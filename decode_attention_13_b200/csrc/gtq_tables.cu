@@ -319,6 +319,8 @@ int tables_for(int device, uint64_t seed, Tables* out) {
   if (e == cudaSuccess) e = up((void**)&t.dec_image, img.data(), img.size() * sizeof(uint32_t));
   if (e == cudaSuccess) e = cudaMalloc((void**)&t.rv_image, b_image_bytes());
   if (e == cudaSuccess) e = build_b_images(t.rot_v, 1, 0, t.rv_image, 0);
+  if (e == cudaSuccess) e = cudaMalloc((void**)&t.rvt_image, b_image_bytes());
+  if (e == cudaSuccess) e = build_b_images(t.rot_vt, 1, 0, t.rvt_image, 0);
   if (e == cudaSuccess) e = cudaMalloc((void**)&t.code_lut, kCodeLutBytes);
   if (e == cudaSuccess) e = build_code_lut(t.thr, t.code_lut, 0);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
