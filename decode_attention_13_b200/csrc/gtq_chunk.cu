@@ -12,9 +12,11 @@
 //     second product.  The reference maximum moves only when it grew by more than
 //     2^8: then the row's output in tensor memory is rescaled (by its own threads,
 //     while no product on it runs).
-//   * warps 8-15       tiles of codes to operands (gtq_dequant.cuh)
-//   * warp 16          tensor memory, issue of all products
-//   * warp 17          bulk copies of the packed tiles and the rotation images
+//     The first warp of each group of four also issues the group's products, as soon as the
+//     group has written its P: one hand-off less than a warp of its own, and 16 warps leave
+//     128 registers each (a 17th costs a quarter of them, and spills in the loop).
+//   * warps 8-15       tiles of codes to operands (gtq_dequant.cuh): keys run two tiles ahead
+//     of values, and a warp's loads of the one are in flight while it works on the other
 // With 129 rows or more (NQ = 2) the two softmax groups take 128 rows each: while
 // one group's products run, the other computes.  With fewer (NQ = 1) they share
 // the rows and take the token blocks in turns, each with an output of its own;
@@ -38,7 +40,7 @@ namespace {
 
 constexpr int kSoftWarps = 8;
 constexpr int kDqWarps = 8;
-constexpr int kChunkThreads = 32 * (kSoftWarps + kDqWarps + 2);
+constexpr int kChunkThreads = 32 * (kSoftWarps + kDqWarps);
 constexpr int kBlockTok = 128;     // tokens of a step
 constexpr int kSplitSlots = 8;     // slots (pairs of coordinates) with a low part
 constexpr float kLog2e = 1.4426950408889634f;
@@ -56,7 +58,7 @@ struct Map {
   static constexpr uint32_t qlo = qhi + NQ * kQHi;
   static constexpr uint32_t k = qlo + NQ * kQLo;
   static constexpr uint32_t v = k + 2 * kKBuf;
-  static constexpr uint32_t tab = v + 3 * kVAtom;
+  static constexpr uint32_t tab = v + 4 * kVAtom;
   static constexpr uint32_t misc = tab + kDqBytes;
   // before the steps: the keys' rotation image; after them: the values' image, then the low
   // parts of the outputs (their high parts lie where the queries were) and, for NQ = 1, the
@@ -69,30 +71,21 @@ struct Map {
 struct Misc {
   alignas(16) HeadMeta m;
   alignas(16) float qscale[kD];
-  uint64_t bar[34];
+  uint64_t bar[16];
   uint32_t tmem;
 };
 
 // barriers
-constexpr int kRing = 4;            // stages of codes at most
-constexpr int kKsFull = 0;          // [kRing] key codes of a tile landed
-constexpr int kKsEmpty = 4;         // [kRing] read
-constexpr int kVsFull = 8;          // [kRing] value codes
-constexpr int kVsEmpty = 12;
-constexpr int kKFull = 16;          // [2] keys of a step written
-constexpr int kKEmpty = 18;         // [2] their products done
-constexpr int kVFull = 20;          // values of a step written
-constexpr int kPvDone = 21;         // the step's second products done
-constexpr int kSFull = 22;          // [2] scores written
-constexpr int kPFull = 24;          // [2] probabilities written
-constexpr int kImg = 26;            // rotation image landed
-constexpr int kQRaw = 27;           // raw queries written
-constexpr int kQRot = 28;           // products of a rotation done
-constexpr int kQFull = 29;          // rotated queries written
-constexpr int kOFull = 30;          // all steps' products done
-constexpr int kOReady = 31;         // outputs written as operands
-constexpr int kDrain = 32;
-constexpr int kNumBars = 33;
+constexpr int kKFull = 0;           // [2] keys of a step written
+constexpr int kKEmpty = 2;          // [2] their products done
+constexpr int kVFull = 4;           // [2] values of a step written
+constexpr int kVEmpty = 6;          // [2] their products done
+constexpr int kSFull = 8;           // [2] scores written
+constexpr int kImg = 10;            // rotation image landed
+constexpr int kQRot = 11;           // products of a rotation done
+constexpr int kQFull = 12;          // rotated queries written
+constexpr int kOFull = 13;          // all steps' products done
+constexpr int kDrain = 14;          // [2] after a failed wait: a group's products so far are done
 
 struct ChunkArgs {
   const uint8_t* packed;
@@ -111,7 +104,6 @@ struct ChunkArgs {
   const uint4* dec_image;
   int row_tiles, splits;
   int64_t span;            // tokens of a split, a multiple of kBlockTok
-  int ks, vs;              // stages of the rings
   float* part_o;           // [heads][splits][rows padded][128]
   float2* part_ml;         // [heads][splits][rows padded]
   int64_t rows_pad;
@@ -190,9 +182,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     return;
   }
   Misc& ms = *reinterpret_cast<Misc*>(sm + M::misc);
-  const uint32_t ring = sb + M::misc + ((sizeof(Misc) + 127) & ~127u);
-  const uint32_t ks_bytes = 1024u * a.kb + 1024u, vs_bytes = 1024u * a.vb + 128u;
-  const uint32_t vring = ring + a.ks * ks_bytes;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int head = blockIdx.y, b = head / a.hkv, h = head % a.hkv;
   const int rt = blockIdx.x % a.row_tiles, sp = blockIdx.x / a.row_tiles;
@@ -226,40 +215,33 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
 
   // ---------------------------------------------------------------- set-up
   if (tid == 0) {
-    for (int i = 0; i < kRing; ++i) {
-      mbar_init(bar(kKsFull + i), 1);
-      mbar_init(bar(kKsEmpty + i), kDqWarps);
-      mbar_init(bar(kVsFull + i), 1);
-      mbar_init(bar(kVsEmpty + i), kDqWarps);
-    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kKFull + i), kDqWarps);
-      mbar_init(bar(kKEmpty + i), 1);
+      mbar_init(bar(kKEmpty + i), NQ);
+      mbar_init(bar(kVFull + i), kDqWarps);
+      mbar_init(bar(kVEmpty + i), NQ);
       mbar_init(bar(kSFull + i), 1);
-      mbar_init(bar(kPFull + i), 4);
+      mbar_init(bar(kDrain + i), 1);
     }
-    mbar_init(bar(kVFull), kDqWarps);
-    mbar_init(bar(kPvDone), 1);
     mbar_init(bar(kImg), 1);
-    mbar_init(bar(kQRaw), 4 * NQ);
-    mbar_init(bar(kQRot), 1);
+    mbar_init(bar(kQRot), NQ);
     mbar_init(bar(kQFull), 4 * NQ);
-    mbar_init(bar(kOFull), 1);
-    mbar_init(bar(kOReady), 4 * NQ);
-    mbar_init(bar(kDrain), 1);
+    mbar_init(bar(kOFull), 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    mbar_expect_tx(bar(kImg), kImage);
+    bulk_load(sb + M::image, a.bimg_k + (size_t)head * kImage, kImage, bar(kImg));
   }
   for (int i = tid; i < (int)(sizeof(HeadMeta) / 4); i += kChunkThreads)
     reinterpret_cast<uint32_t*>(&ms.m)[i] = reinterpret_cast<const uint32_t*>(a.meta + head)[i];
   load_dequant_tables(sm + M::tab, a.dec_image, tid, kChunkThreads);
-  if (warp == 16) {
+  if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(&ms.tmem)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ms.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ms.tmem, 0);  // the same in all lanes, and known to be
   // log2(e) / (sqrt(d) sqrt(m)) and the keys' factor 1 / 8 undone
   if (tid < kD)
     ms.qscale[tid] = (tid >> 1) < ms.m.n_slots
@@ -270,7 +252,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
 
   if (warp < kSoftWarps) {
     // -------------------------------------------------------------- softmax
-    const int grp = warp >> 2, lrow = (warp & 3) * 32 + lane;  // row within its 128
+    const int grp = __shfl_sync(0xffffffffu, warp >> 2, 0), lrow = (warp & 3) * 32 + lane;  // row within its 128
+    const bool issuer = __shfl_sync(0xffffffffu, (int)((warp & 3) == 0), 0);
     const int tile = NQ == 2 ? grp : 0;
     const int64_t row = r0 + 128 * tile + lrow;
     const bool mine = row < n_rows;
@@ -281,6 +264,43 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     const uint32_t t_s = tmem + lane_off + 128u * grp, t_o = tmem + lane_off + 256u + 128u * grp;
     uint8_t* qhi = sm + M::qhi + tile * kQHi + lrow * 128;
     const uint32_t sw = (uint32_t)(lrow & 7);
+    // A wait that has failed is not repeated, but every barrier of the group is still met.
+    auto waits = [&](int i, uint32_t par) {
+      if (!failed && !mbar_wait(bar(i), par)) failed = 1;
+      __syncwarp();
+    };
+    auto group_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(2 + grp) : "memory"); };
+    // products of the group, issued by one lane of its first warp; a descriptor's start moves by
+    // adding to the low word
+    const uint32_t idc = idesc_f16(128);
+    auto step_of = [](uint32_t ks) { return (uint64_t)(((ks >> 2) * 16384 + (ks & 3) * 32) >> 4); };
+    const uint32_t d_s = tmem + 128u * grp, d_o = tmem + 256u + 128u * grp;
+    auto rotate = [&](uint32_t x, bool more, bool with_lo) {
+      // scores (+)= x . (hi + lo)^T of the image (with_lo), or x . hi^T
+      const uint64_t dx = smem_desc(sb + x), di = smem_desc(sb + M::image);
+#pragma unroll 1
+      for (int part = 0; part < (with_lo ? 2 : 1); ++part)
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          tc_mma(d_s, dx + step_of(ks), di + step_of(ks) + part * (32768 >> 4), idc, more || (part | ks) != 0);
+    };
+    auto scores = [&](int j) {
+      const uint64_t dq = smem_desc(sb + M::qhi + tile * kQHi), dk = smem_desc(sb + M::k + (j & 1) * kKBuf);
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) tc_mma(d_s, dq + step_of(ks), dk + step_of(ks), idc, ks != 0);
+      tc_mma(d_s, smem_desc_plain(sb + M::qlo + tile * kQLo, 128, 256), dk, idc, 1);
+      tc_mma(d_s, dq, smem_desc_plain(sb + M::k + (j & 1) * kKBuf + 32768, 128, 256), idc, 1);
+      tc_commit(bar(kSFull + grp));
+      tc_commit(bar(kKEmpty + (j & 1)));
+    };
+    auto outputs = [&](int j, bool more) {
+      const uint64_t dv = smem_desc(sb + M::v + (j & 1) * 2 * kVAtom);
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks)
+        tc_mma_ta(d_o, d_s + 8u * ks, dv + (uint64_t)(((ks >> 2) * kVAtom + (ks & 3) * 32) >> 4), idc, more || ks != 0);
+      tc_commit(bar(kVEmpty + (j & 1)));
+    };
+    const int first = NQ == 2 ? 0 : grp, stride = NQ == 2 ? 1 : 2;  // the group's steps
     // raw queries -> operand, rotated by the tensor cores, back as scaled hi + lo
     if (NQ == 2 || grp == 0) {
       const uint4* src = reinterpret_cast<const uint4*>(a.q + b * a.qs[0] + hq * a.qs[1] + tok * a.qs[2]);
@@ -290,10 +310,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         *reinterpret_cast<uint4*>(qhi + (c >> 3) * 16384 + (((c & 7) ^ sw) << 4)) = v;
       }
       fence_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kQRaw));
-      if (!mbar_wait(bar(kQRot), 0)) failed = 1;
-      __syncwarp();
+      group_sync();
+      if (issuer) {
+        waits(kImg, 0);
+        tc_fence_after();
+        if (elect_one() && !failed) {
+          rotate(M::qhi + tile * kQHi, false, true);
+          tc_commit(bar(kQRot));
+        }
+        __syncwarp();
+      }
+      waits(kQRot, 0);
       tc_fence_after();
       uint8_t* qlo = sm + M::qlo + tile * kQLo + (lrow >> 3) * 256 + (lrow & 7) * 16;
 #pragma unroll 1
@@ -331,9 +358,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     if (end > s1) end = s1;
     float ref = -INFINITY, sum = 0.f;
     int it = 0;
-    for (int j = NQ == 2 ? 0 : grp; j < nb && !failed; j += NQ == 2 ? 1 : 2, ++it) {
-      if (!mbar_wait(bar(kSFull + grp), it & 1)) { failed = 1; break; }
+    if (issuer && first < nb) {  // the first scores
+      waits(kQFull, 0);
+      waits(kKFull + (first & 1), 0);
+      tc_fence_after();
+      if (elect_one() && !failed) scores(first);
       __syncwarp();
+    }
+#pragma unroll 1
+    for (int j = first; j < nb; j += stride, ++it) {
+      waits(kSFull + grp, it & 1);
       tc_fence_after();
       if (warp_on) {
         const int64_t left = end - (s0 + (int64_t)j * kBlockTok);
@@ -363,13 +397,31 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         sum += whole ? row_exp<false>(t_s, cnt, base) : row_exp<true>(t_s, cnt, base);
       }
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kPFull + grp));
+      group_sync();
+      if (issuer) {
+        waits(kVFull + (j & 1), (j >> 1) & 1);
+        tc_fence_after();
+        const int nj = j + stride;
+        if (elect_one() && !failed) outputs(j, it > 0);
+        __syncwarp();
+        if (nj < nb) {
+          waits(kKFull + (nj & 1), (nj >> 1) & 1);
+          tc_fence_after();
+          if (elect_one() && !failed) scores(nj);
+          __syncwarp();
+        }
+      }
     }
-    // outputs: normalised, split into hi + lo operands of the last product
-    if (!mbar_wait(bar(kOFull), 0)) failed = 1;
+    if (issuer && elect_one()) tc_commit(bar(kOFull));
     __syncwarp();
+    // outputs: normalised, split into hi + lo operands of the last product
+    waits(kOFull, 0);
     tc_fence_after();
+    if (warp == 0 && lane == 0 && !failed) {  // the operands' memory is free: the values' rotation
+      mbar_expect_tx(bar(kImg), kImage);
+      bulk_load(sb + M::image, a.img_vt, kImage, bar(kImg));
+    }
+    __syncwarp();
     float total = sum, top = ref, other = 0.f;
     float own = 1.f;
     float2* stat = reinterpret_cast<float2*>(sm + M::stat);
@@ -426,10 +478,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       }
       tc_fence_before();
       fence_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kOReady));
-      if (!mbar_wait(bar(kQRot), 1)) failed = 1;
-      __syncwarp();
+      group_sync();
+      if (issuer) {
+        waits(kImg, 1);
+        tc_fence_after();
+        if (elect_one() && !failed) {
+          rotate(M::qhi + tile * kQHi, false, true);
+          rotate(M::olo + tile * 32768, true, false);
+          tc_commit(bar(kQRot));
+        }
+        __syncwarp();
+      }
+      waits(kQRot, 1);
       tc_fence_after();
       if (warp_on && !__any_sync(0xffffffffu, failed)) {
         const bool split = a.splits > 1;
@@ -461,199 +521,119 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         if (split && mine) a.part_ml[slot0 + 128 * tile + lrow] = make_float2(top, total);
       }
     }
-  } else if (warp < kSoftWarps + kDqWarps) {
+  } else {
     // ------------------------------------------------------ codes to operands
     const int dw = warp - kSoftWarps;
     const uint32_t tab = sb + M::tab;
-    const HeadMeta& m = ms.m;
+    // quads dw and 15 - dw of the keys, dims 16 dw .. of the values, of every tile
+    const uint32_t norms = key_norm_offset(a.kb, a.vb);
+    const KeyLane k0 = key_lane(ms.m, dw, lane, 16384, norms), k1 = key_lane(ms.m, 15 - dw, lane, 16384, norms);
+    const bool low = dw < kSplitSlots / 4;  // slots of quad dw leave low parts
+    const uint32_t lo_lane = (uint32_t)dw * 128 + 16u * (lane & 7) + 4u * (lane >> 3);
+    const bool code0 = low || __any_sync(0xffffffffu, k0.w > 4), code1 = __any_sync(0xffffffffu, k1.w > 4);
+    // tile addresses: page numbers are read a tile ahead of their use
+    const int64_t t0 = s0 / kTile;
+    const uint8_t* const base = a.packed + (a.sm.table ? (int64_t)h * a.sm.tile_bytes
+                                                       : ((int64_t)head * a.sm.n_tiles + t0) * a.sm.tile_bytes);
+    const int32_t* const pages = a.sm.table ? a.sm.table + (int64_t)b * a.sm.max_blocks + t0 : nullptr;
+    int page = pages ? __ldg(pages) : 0;
+    auto tile_at = [&](int t) {  // called once for every t < nt in order
+      const uint8_t* p = base + (pages ? (int64_t)page * a.sm.hkv : (int64_t)t) * a.sm.tile_bytes;
+      if (pages && t + 1 < nt) page = __ldg(pages + t + 1);
+      return p;
+    };
+    KeyRaw r0, r1;
+    ValueRaw rv;
+    auto fetch_keys = [&](const uint8_t* p) {
+      if (code0) load_keys<5>(r0, p, k0);
+      else load_keys<2>(r0, p, k0);
+      if (!code1) load_keys<2>(r1, p, k1);
+    };
+    auto put_keys = [&](int t, const uint8_t* p) {
+      const uint32_t dst = sb + M::k + ((t >> 1) & 1) * kKBuf, row = dst + (t & 1) * 8192;
+      if (code0) keys_by_code(k0, r0, tab, row, low, dst + 32768 + (t & 1) * 2048 + lo_lane, 256);
+      else keys_by_pair(k0, r0, tab, 4u * lane, row);
+      if (!code1) {
+        keys_by_pair(k1, r1, tab, 4u * lane, row);
+      } else {  // widths above 4 beyond the first half of the slots: fetched when they are due
+        KeyRaw r;
+        load_keys<5>(r, p, k1);
+        keys_by_code(k1, r, tab, row, false, 0, 0);
+      }
+    };
+    const uint8_t *pa = tile_at(0), *pb = nullptr, *pc = nullptr;  // tiles v, v + 1, v + 2
+    fetch_keys(pa);
     // the keys' buffers lie under the rotation image
     if (!mbar_wait(bar(kQRot), 0)) failed = 1;
-    auto keys = [&](int j) {  // keys of step j
-      if (j >= 2 && !mbar_wait(bar(kKEmpty + (j & 1)), ((j >> 1) & 1) ^ 1)) return false;
-      const uint32_t dst = sb + M::k + (j & 1) * kKBuf;
-      for (int half = 0; half < 2; ++half) {
-        const int t = 2 * j + half;
-        if (t >= nt) break;  // rows behind the last tile: whatever they hold, their scores do not count
-        const int st = t % a.ks;
-        if (!mbar_wait(bar(kKsFull + st), (t / a.ks) & 1)) return false;
-        const uint32_t src = ring + st * ks_bytes;
-        // the quads with low parts cost more: they go round the warps
-        for (int k = 0; k < 2; ++k)
-          dequant_keys(m, ((dw + t) & 7) + 8 * k, lane, src, src + 1024u * a.kb, tab, dst + half * 8192, 16384,
-                       kSplitSlots, dst + 32768 + half * 2048, 256);
+    __syncwarp();
+    // step by step: keys of tile t = v + 2, then values of tile v
+#pragma unroll 1
+    for (int t = 0; t < 2 * nb + 2 && !failed; ++t) {
+      const int v = t - 2;
+      const uint8_t* now = t == 0 ? pa : (t == 1 ? pb : pc);
+      if (v >= 0 && v < nt) load_values(rv, pa, a.kb, a.vb, dw, lane);
+      if (t < 2 * nb) {
+        const int j = t >> 1;
+        if (!(t & 1) && j >= 2 && !mbar_wait(bar(kKEmpty + (j & 1)), ((j >> 1) & 1) ^ 1)) { failed = 1; break; }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kKsEmpty + st));
-      }
-      fence_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kKFull + (j & 1)));
-      return true;
-    };
-    auto values = [&](int j) {
-      for (int half = 0; half < 2; ++half) {
-        const int t = 2 * j + half;
-        // three atoms: the second of a step is the one that the step before began with
-        if (half == 1 && j >= 1 && !mbar_wait(bar(kPvDone), (j - 1) & 1)) return false;
-        const uint32_t dst = sb + M::v + (t % 3) * kVAtom;
-        if (t < nt) {
-          const int st = t % a.vs;
-          if (!mbar_wait(bar(kVsFull + st), (t / a.vs) & 1)) return false;
-          const uint32_t src = vring + st * vs_bytes;
-          const int64_t left = s1 - (s0 + (int64_t)t * kTile);
-          uint32_t n[8];
-          value_norms(src + 1024u * a.vb, lane, left < kTile ? (int)left : kTile, n);
-          dequant_values(a.vb, dw, lane, src, n, tab, dst);
+        // rows behind the last tile: whatever they hold, their scores do not count
+        if (t < nt) put_keys(t, now);
+        if (t & 1) {
+          fence_async();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kVsEmpty + st));
+          if (lane == 0) mbar_arrive(bar(kKFull + (j & 1)));
+        }
+      }
+      // the next tile's keys, in flight during the values
+      const uint8_t* next = t + 1 < nt ? tile_at(t + 1) : nullptr;
+      if (next) fetch_keys(next);
+      if (v >= 0) {
+        const int j = v >> 1;
+        if (!(v & 1) && j >= 2 && !mbar_wait(bar(kVEmpty + (j & 1)), ((j >> 1) & 1) ^ 1)) { failed = 1; break; }
+        __syncwarp();
+        const uint32_t atom = M::v + (v & 3) * kVAtom;
+        if (v < nt) {
+          const int64_t left = s1 - (s0 + (int64_t)v * kTile);
+          uint32_t n[8];
+          value_norms(rv, lane, left < kTile ? (int)left : kTile, n);
+          dequant_values(pa, a.kb, a.vb, dw, lane, rv, n, tab, sb + atom);
         } else {  // no tile: zeros, since the probabilities' zeros must not meet a NaN
           for (int i = lane; i < 128; i += 32)
-            *reinterpret_cast<uint4*>(sm + M::v + (t % 3) * kVAtom + dw * 2048 + 16 * i) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(sm + atom + dw * 2048 + 16 * i) = make_uint4(0, 0, 0, 0);
         }
-      }
-      fence_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kVFull));
-      return true;
-    };
-    if (!failed && !keys(0)) failed = 1;
-    for (int j = 0; j < nb && !failed; ++j) {
-      if (j + 1 < nb && !keys(j + 1)) { failed = 1; break; }
-      if (!values(j)) { failed = 1; break; }
-    }
-  } else if (warp == 16) {
-    // ------------------------------------------------------------- products
-    if (lane == 0) {
-      const uint32_t idc = idesc_f16(128);
-      auto rotate = [&](uint32_t d, uint32_t x, uint32_t img, bool more, bool with_lo) {
-        // d (+)= x . (hi + lo)^T of the image; with_lo: the low part of the image too
-#pragma unroll
-        for (int part = 0; part < 2; ++part)
-          if (part == 0 || with_lo)
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-              const uint32_t o = (ks >> 2) * 16384 + (ks & 3) * 32;
-              tc_mma(d, smem_desc(x + o), smem_desc(img + part * 32768 + o), idc, more || (part | ks) != 0);
-            }
-      };
-      auto scores = [&](int x, int j) {
-        const uint32_t qt = NQ == 2 ? x : 0;
-        const uint32_t q = sb + M::qhi + qt * kQHi, k = sb + M::k + (j & 1) * kKBuf, d = tmem + 128u * x;
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          const uint32_t o = (ks >> 2) * 16384 + (ks & 3) * 32;
-          tc_mma(d, smem_desc(q + o), smem_desc(k + o), idc, ks != 0);
+        if (v & 1) {
+          fence_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kVFull + (j & 1)));
         }
-        tc_mma(d, smem_desc_plain(sb + M::qlo + qt * kQLo, 128, 256), smem_desc(k), idc, 1);
-        tc_mma(d, smem_desc(q), smem_desc_plain(k + 32768, 128, 256), idc, 1);
-        tc_commit(bar(kSFull + x));
-      };
-      auto outputs = [&](int x, int j, bool more) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t v = sb + M::v + ((2 * j + half) % 3) * kVAtom;
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            tc_mma_ta(tmem + 256u + 128u * x, tmem + 128u * x + 32u * half + 8u * ks, smem_desc(v + 32 * ks), idc,
-                      more || (half | ks) != 0);
-        }
-      };
-      auto waits = [&](int i, uint32_t par) {
-        if (!failed && !mbar_wait(bar(i), par)) failed = 1;
-        return !failed;
-      };
-      waits(kImg, 0);
-      if (waits(kQRaw, 0)) {
-        tc_fence_after();
-        for (int x = 0; x < NQ; ++x) rotate(tmem + 128u * x, sb + M::qhi + x * kQHi, sb + M::image, false, true);
-        tc_commit(bar(kQRot));
-      }
-      waits(kQFull, 0);
-      // first scores
-      for (int x = 0; x < 2 && !failed; ++x) {
-        const int j = NQ == 2 ? 0 : x;
-        if (j >= nb || !waits(kKFull + (j & 1), 0)) break;
-        tc_fence_after();
-        scores(x, j);
-        if (NQ == 1 || x == 1) tc_commit(bar(kKEmpty + (j & 1)));
-      }
-      for (int j = 0; j < nb && !failed; ++j) {
-        for (int y = 0; y < NQ; ++y) {
-          const int x = NQ == 2 ? y : j & 1;           // group
-          const int it = NQ == 2 ? j : j >> 1;         // its step
-          const int nj = NQ == 2 ? j + 1 : j + 2;      // its next
-          if (!waits(kPFull + x, it & 1) || !waits(kVFull, j & 1)) break;
-          tc_fence_after();
-          outputs(x, j, it > 0);
-          if (y == NQ - 1) tc_commit(bar(kPvDone));
-          if (nj < nb) {
-            if (!waits(kKFull + (nj & 1), (nj >> 1) & 1)) break;
-            tc_fence_after();
-            scores(x, nj);
-            if (y == NQ - 1) tc_commit(bar(kKEmpty + (nj & 1)));
-          }
-        }
-      }
-      tc_commit(bar(kOFull));
-      if (waits(kImg, 1) && waits(kOReady, 0)) {
-        tc_fence_after();
-        const uint32_t img = sb + M::image;
-        for (int x = 0; x < NQ; ++x) {
-          rotate(tmem + 128u * x, sb + M::qhi + x * kQHi, img, false, true);
-          rotate(tmem + 128u * x, sb + M::olo + x * 32768, img, true, false);
-        }
-        tc_commit(bar(kQRot));
-      }
-    }
-  } else {
-    // ------------------------------------------------------------ bulk copies
-    if (lane == 0) {
-      mbar_expect_tx(bar(kImg), kImage);
-      bulk_load(sb + M::image, a.bimg_k + (size_t)head * kImage, kImage, bar(kImg));
-      const uint32_t norm_bytes = 128u * ms.m.n_groups;
-      const int64_t t0 = s0 / kTile;
-      int kt = 0, vt = 0;  // next tile of each ring
-      while ((kt < nt || vt < nt) && !failed) {
-        // keys run a step (and the next step's two tiles) ahead of the values, as they are used: a
-        // ring of one stage still never waits for a tile that is behind it
-        const bool key = kt < nt && (kt < vt + 4 || vt >= nt);
-        const int t = key ? kt : vt, n = key ? a.ks : a.vs, st = t % n;
-        if (t >= n && !mbar_wait(bar((key ? kKsEmpty : kVsEmpty) + st), ((t / n) & 1) ^ 1)) { failed = 1; break; }
-        const uint8_t* src = a.sm.tile(const_cast<uint8_t*>(a.packed), head, t0 + t);
-        if (key) {
-          const uint32_t dst = ring + st * ks_bytes;
-          mbar_expect_tx(bar(kKsFull + st), 1024u * a.kb + norm_bytes);
-          bulk_load(dst, src, 1024u * a.kb, bar(kKsFull + st));
-          if (norm_bytes)
-            bulk_load(dst + 1024u * a.kb, src + key_norm_offset(a.kb, a.vb), norm_bytes, bar(kKsFull + st));
-          ++kt;
-        } else {
-          mbar_expect_tx(bar(kVsFull + st), vs_bytes);
-          bulk_load(vring + st * vs_bytes, src + 1024u * a.kb, vs_bytes, bar(kVsFull + st));
-          ++vt;
-        }
-      }
-      if (!mbar_wait(bar(kOFull), 0)) failed = 1;
-      if (!failed) {
-        mbar_expect_tx(bar(kImg), kImage);
-        bulk_load(sb + M::image, a.img_vt, kImage, bar(kImg));
-        if (!mbar_wait(bar(kImg), 1)) failed = 1;
-      } else {  // copies in flight: the image, and the last of every stage
-        mbar_wait(bar(kImg), 0);
-        for (int i = 0; i < a.ks && i < kt; ++i) mbar_wait(bar(kKsFull + i), ((kt - 1 - i) / a.ks) & 1);
-        for (int i = 0; i < a.vs && i < vt; ++i) mbar_wait(bar(kVsFull + i), ((vt - 1 - i) / a.vs) & 1);
+        pa = pb;
+        pb = pc;
+        pc = next;
+      } else if (t == 0) {
+        pb = next;
+      } else {
+        pc = next;
       }
     }
   }
   if (failed) atomicOr(a.status, kStatusTimeout);
+  // After a failed wait, nothing in flight may outlive the block: each issuer waits (bounded) for
+  // its products so far, and the images' copies are waited for.
   if (__syncthreads_or(failed)) {
-    if (warp == 16 && lane == 0) {
-      tc_commit(bar(kDrain));
-      mbar_wait(bar(kDrain), 0);
+    if (warp == 0 || warp == 4) {
+      if (elect_one()) {  // the lane that issued them
+        tc_commit(bar(kDrain + (warp >> 2)));
+        mbar_wait(bar(kDrain + (warp >> 2)), 0);
+      }
+    }
+    if (tid == 0) {
+      mbar_wait(bar(kImg), 0);
+      mbar_wait(bar(kImg), 1);
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 16) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
 // One warp per row: the splits' outputs, weighted by what their maxima and sums say.
@@ -687,40 +667,24 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Chun
       make_uint2(pack_h2(acc.x * inv, acc.y * inv), pack_h2(acc.z * inv, acc.w * inv));
 }
 
-// How a call is cut: rows per block, splits of the tokens, stages.
+// How a call is cut: rows per block and splits of the tokens.
 struct Cut {
-  int nq, row_tiles, splits, ks, vs;
+  int nq, row_tiles, splits;
   int64_t span, rows_pad;
   uint32_t smem;
 };
 
-constexpr uint32_t kSmemMost = 232448;
-constexpr uint32_t kMiscBytes = (uint32_t)((sizeof(Misc) + 127) & ~127u);
-static_assert(Map<1>::misc + kMiscBytes + (1024 * 8 + 1024) + (1024 * 8 + 128) <= kSmemMost, "widest codes");
+template <int NQ>
+constexpr uint32_t smem_of() {
+  return Map<NQ>::misc + (uint32_t)sizeof(Misc);
+}
+static_assert(smem_of<2>() <= 232448, "shared memory of a block");
 
 Cut cut_of(const gtq_plan* p, int64_t T, int64_t n) {
   Cut c;
   const int64_t rows = n * p->g_q;
-  const uint32_t kbytes = 1024u * p->cfg.k_bits + 1024u, vbytes = 1024u * p->cfg.v_bits + 128u;
-  auto room = [&](int nq) {
-    return (int)kSmemMost - (int)((nq == 2 ? Map<2>::misc : Map<1>::misc) + kMiscBytes);
-  };
-  // 256 rows a block where there are that many and two tiles of keys and one of values fit beside
-  // them (up to 8 bits a dim for both together); then as many tiles in flight as fit
-  c.nq = rows > 128 && room(2) >= (int)(2 * kbytes + vbytes) ? 2 : 1;
-  c.ks = c.vs = 1;
-  for (bool more = true; more;) {
-    more = false;
-    if (c.ks < kRing && c.ks <= c.vs && room(c.nq) >= (int)((c.ks + 1) * kbytes + c.vs * vbytes)) {
-      ++c.ks;
-      more = true;
-    }
-    if (c.vs < kRing && room(c.nq) >= (int)(c.ks * kbytes + (c.vs + 1) * vbytes)) {
-      ++c.vs;
-      more = true;
-    }
-  }
-  c.smem = (c.nq == 2 ? Map<2>::misc : Map<1>::misc) + kMiscBytes + c.ks * kbytes + c.vs * vbytes;
+  c.nq = rows > 128 ? 2 : 1;
+  c.smem = c.nq == 2 ? smem_of<2>() : smem_of<1>();
   c.row_tiles = (int)((rows + 128 * c.nq - 1) / (128 * c.nq));
   c.rows_pad = (int64_t)c.row_tiles * 128 * c.nq;
   // Splits: enough blocks to fill the SMs, and evenly; a block's set-up and end cost about as
@@ -780,8 +744,6 @@ cudaError_t launch_chunk(const gtq_plan* p, const uint8_t* packed, int64_t T, co
   a.row_tiles = c.row_tiles;
   a.splits = c.splits;
   a.span = c.span;
-  a.ks = c.ks;
-  a.vs = c.vs;
   a.rows_pad = c.rows_pad;
   a.status = p->d_status;
   const size_t slots = (size_t)p->n_heads * c.splits * c.rows_pad;

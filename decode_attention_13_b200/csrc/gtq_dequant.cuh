@@ -11,8 +11,11 @@
 // Powers of two keep the largest norm (65504) times the largest centroid in the
 // fp16 range; both are undone in the queries and at the end.
 //
-// A pair of codes is looked up at once where the pair table is small (widths 1
-// to 3: one 32-bit copy per lane, no bank conflicts), code by code above.
+// Keys of widths up to 4 take a pair of codes in one lookup, every lane by its own
+// width (mask, table, multiplier), so that four slots of different widths run as
+// one instruction stream: straight-line code per width measured 2.5 times slower,
+// waiting for instructions.  Wider codes, and slots that leave a low part, are
+// looked up one by one in a loop.
 #pragma once
 
 #include "gtq_internal.h"
@@ -20,46 +23,52 @@
 
 namespace gtq {
 
-// Lookup tables in shared memory: pair tables of widths 3, 2, 1 and the single
-// codes of width 5 as they lie in the decode image (kTabP32W3 .. kTabS32W6),
-// single codes of width 4 (one copy per lane), single codes of all widths.
+// Lookup tables in shared memory (fp16 values of the codebook): pair tables of
+// widths 3, 2, 1 with a copy per lane, as they lie in the decode image (kTabP32W3
+// .. kTabS32W5), a pair table of width 4 in one copy, single codes of all widths
+// (kTabSS: hi | lo << 16), and a zero.
 constexpr uint32_t kDqPairs = 0;
-constexpr uint32_t kDqPairBytes = kTabS32W6 - kTabP32W3;
-constexpr uint32_t kDqW4 = kDqPairs + kDqPairBytes;
-constexpr uint32_t kDqSingles = kDqW4 + (16u << 7);
-constexpr uint32_t kDqBytes = kDqSingles + 2048u;
-static_assert(kDqBytes % 16 == 0, "dequantisation tables");
+constexpr uint32_t kDqPairBytes = kTabS32W5 - kTabP32W3;
+constexpr uint32_t kDqPair4 = kDqPairs + kDqPairBytes;
+constexpr uint32_t kDqSingles = kDqPair4 + 1024u;
+constexpr uint32_t kDqZero = kDqSingles + 2048u;
+constexpr uint32_t kDqBytes = kDqZero + 128u;
+static_assert(kDqBytes % 128 == 0, "dequantisation tables");
 
 // Copies the tables from the decode image (all threads of the block).
 __device__ __forceinline__ void load_dequant_tables(uint8_t* tab, const uint4* image, int tid,
                                                     int n_threads) {
   const uint8_t* img = reinterpret_cast<const uint8_t*>(image);
+  const uint32_t* ss = reinterpret_cast<const uint32_t*>(img + kTabSS);
   for (int i = tid; i < (int)(kDqPairBytes / 16); i += n_threads)
     reinterpret_cast<uint4*>(tab + kDqPairs)[i] = reinterpret_cast<const uint4*>(img + kTabP32W3)[i];
-  for (int i = tid; i < 512; i += n_threads) {
-    const uint32_t* ss = reinterpret_cast<const uint32_t*>(img + kTabSS);
-    reinterpret_cast<uint32_t*>(tab + kDqSingles)[i] = ss[i];
-    reinterpret_cast<uint32_t*>(tab + kDqW4)[i] = ss[kSingleOff(4) / 4 + (i >> 5)];
-  }
+  for (int i = tid; i < 512; i += n_threads) reinterpret_cast<uint32_t*>(tab + kDqSingles)[i] = ss[i];
+  for (int i = tid; i < 256; i += n_threads)
+    reinterpret_cast<uint32_t*>(tab + kDqPair4)[i] =
+        __byte_perm(ss[kSingleOff(4) / 4 + (i & 15)], ss[kSingleOff(4) / 4 + (i >> 4)], 0x5410);
+  if (tid < 32) reinterpret_cast<uint32_t*>(tab + kDqZero)[tid] = 0;
 }
 
+// From the lookup tables, which never change: the compiler may move it anywhere.
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
   asm("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
+// Codes and norms from the cache.  Volatile: the compiler may not move these loads to their use,
+// a whole tile later (it did, and every tile then waited for the memory).
+__device__ __forceinline__ uint32_t ldg32(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 ldg128(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
 __device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
-  asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-}
-__device__ __forceinline__ uint32_t h2mul(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint32_t h2fma(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v));
 }
 
 // Bits [P, P + N) of the word array x, moved to bits [S, S + N) of the result
@@ -77,186 +86,206 @@ __device__ __forceinline__ uint32_t field(const uint32_t* x) {
   }
 }
 
-// 16 W bits from byte address `a` (a multiple of 2; of 4 for even W) in shared
-// memory, in words.
-template <int W>
-__device__ __forceinline__ void load_portion(uint32_t a, uint32_t (&x)[5]) {
-  if constexpr (W == 8) {
-    asm("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(a));
-  } else if constexpr (W == 4) {
-    asm("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(a));
-  } else if constexpr (W % 2 == 0) {
-#pragma unroll
-    for (int i = 0; i < W / 2; ++i) x[i] = lds32(a + 4 * i);
-  } else {  // an odd number of halfwords that starts at either half of a word
-    constexpr int n = (W + 1) / 2;
-    const uint32_t base = a & ~3u, sh = (a & 2u) * 8u;
-    uint32_t y[n + 1];
-#pragma unroll
-    for (int i = 0; i < n; ++i) y[i] = lds32(base + 4 * i);
-    y[n] = 0;
-#pragma unroll
-    for (int i = 0; i < n; ++i) x[i] = __funnelshift_r(y[i], y[i + 1], sh);
-  }
-}
-
-// Entry (fp16 hi | lo << 16) of code I of width W in the words x.
-template <int W, int I, bool SHARED>
-__device__ __forceinline__ uint32_t single(const uint32_t* x, uint32_t tab, uint32_t lane4) {
-  if constexpr (!SHARED && W == 4)
-    return lds32(tab + kDqW4 + (field<I * 4, 4, 7>(x) | lane4));
-  else if constexpr (!SHARED && W == 5) {
-    // the place that a field of 5 bits moves to must not lie above where it starts
-    // in a crossing word: 7 only below bit 28, which always holds for a crossing
-    return lds32(tab + kDqPairs + (kTabS32W5 - kTabP32W3) + (field<I * 5, 5, 7>(x) | lane4));
-  } else
-    return lds32(tab + kDqSingles + kSingleOff(W) + field<I * W, W, 2>(x));
+// Code I of width W in the words x: its entry (fp16 hi | lo << 16).
+template <int W, int I>
+__device__ __forceinline__ uint32_t single(const uint32_t* x, uint32_t tab) {
+  return lds32(tab + kDqSingles + kSingleOff(W) + field<I * W, W, 2>(x));
 }
 
 // fp16 pair (codes 2 U, 2 U + 1 of width W), hi parts.
 template <int W, int U>
 __device__ __forceinline__ uint32_t code_pair_hi(const uint32_t* x, uint32_t tab, uint32_t lane4) {
-  if constexpr (W <= 3) {
+  if constexpr (W <= 3)
     return lds32(tab + kDqPairs + (kTabP32(W) - kTabP32W3) + (field<2 * U * W, 2 * W, 7>(x) | lane4));
-  } else {
-    const uint32_t e0 = single<W, 2 * U, (W > 5)>(x, tab, lane4);
-    const uint32_t e1 = single<W, 2 * U + 1, (W > 5)>(x, tab, lane4);
-    return __byte_perm(e0, e1, 0x5410);
-  }
+  else if constexpr (W == 4)
+    return lds32(tab + kDqPair4 + field<8 * U, 8, 2>(x));
+  else
+    return __byte_perm(single<W, 2 * U>(x, tab), single<W, 2 * U + 1>(x, tab), 0x5410);
 }
 
-// norm u (0..7) of four words of fp16 pairs, in both halves
-template <int U>
-__device__ __forceinline__ uint32_t norm_both(const uint32_t* n) {
-  return __byte_perm(n[U >> 1], 0, (U & 1) ? 0x3232 : 0x1010);
-}
+__device__ __forceinline__ __half2 as_h2(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
+__device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
 
-// One slot's portion: 8 tokens (rows g + 8 u of `dst`, 128 bytes a row, 1024 a
-// group of 8), the pair at byte `col` of the (already swizzled) row.
-template <int W, int U>
-__device__ __forceinline__ void key_pairs(const uint32_t* x, const uint32_t* n, uint32_t tab,
-                                          uint32_t lane4, uint32_t dst) {
-  sts32(dst + 1024 * U, h2mul(code_pair_hi<W, U>(x, tab, lane4), norm_both<U>(n)));
-  if constexpr (U < 7) key_pairs<W, U + 1>(x, n, tab, lane4, dst);
-}
-// The same with the rest of the product beyond its fp16 value, in plain layout.
-template <int W, int U>
-__device__ __forceinline__ void key_pairs_split(const uint32_t* x, const uint32_t* n, uint32_t tab,
-                                                uint32_t dst, uint32_t dst_lo, uint32_t lo_step) {
-  const uint32_t e0 = single<W, 2 * U, true>(x, tab, 0), e1 = single<W, 2 * U + 1, true>(x, tab, 0);
-  const uint32_t hi = __byte_perm(e0, e1, 0x5410), lo = __byte_perm(e0, e1, 0x7632);
-  const uint32_t nn = norm_both<U>(n);
-  const uint32_t p = h2mul(hi, nn);
-  sts32(dst + 1024 * U, p);
-  // hi * n - fp16(hi * n) is exact in one fma (above the subnormals); lo * n joins it
-  sts32(dst_lo + lo_step * U, h2fma(lo, nn, h2fma(hi, nn, p ^ 0x80008000u)));
-  if constexpr (U < 7) key_pairs_split<W, U + 1>(x, n, tab, dst, dst_lo, lo_step);
-}
-
-template <int W>
-__device__ __forceinline__ void key_slot(uint32_t src, uint32_t src_norm, uint32_t tab,
-                                         uint32_t lane4, uint32_t dst, bool split, uint32_t dst_lo,
-                                         uint32_t lo_step) {
-  uint32_t x[5], n[4];
-  load_portion<W>(src, x);
-  asm("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(n[0]), "=r"(n[1]), "=r"(n[2]), "=r"(n[3]) : "r"(src_norm));
-#pragma unroll
-  for (int i = 0; i < 4; ++i) n[i] = h2mul(n[i], 0x30003000u);  // 1 / 8
-  if (split) key_pairs_split<W, 0>(x, n, tab, dst, dst_lo, lo_step);
-  else key_pairs<W, 0>(x, n, tab, lane4, dst);
-}
-
-// Four slots (4 quad .. 4 quad + 3) of a tile: `codes` and `norms` are the
-// shared addresses of the tile's key codes and key norms, `dst` the tile's first
-// row in the operand's first atom (the second one `atom` bytes on).  Slots below
-// n_split also leave the products' rests at dst_lo, in core matrices of 8 rows x 16
-// bytes: row r, coordinate c at (r / 8) * lo_rows + (c / 8) * 128 + (r % 8) * 16 +
-// (c % 8) * 2.
-__device__ __forceinline__ void dequant_keys(const HeadMeta& m, int quad, int lane, uint32_t codes,
-                                             uint32_t norms, uint32_t tab, uint32_t dst,
-                                             uint32_t atom, int n_split, uint32_t dst_lo,
-                                             uint32_t lo_rows) {
+// A lane's slot among four (4 quad .. 4 quad + 3) of a tile's keys.
+struct KeyLane {
+  uint32_t src;      // byte offset of its portion in the tile
+  uint32_t sn;       // of its norms
+  uint32_t col;      // of its pair in the operand: row g, swizzled column
+  uint32_t w;        // width (0: no code)
+};
+__device__ __forceinline__ KeyLane key_lane(const HeadMeta& m, int quad, int lane, uint32_t atom,
+                                            uint32_t norms) {
   const int g = lane & 7, s = 4 * quad + (lane >> 3);
-  const uint32_t lane4 = 4u * (uint32_t)lane;
-  const uint32_t col = (uint32_t)((((s >> 2) & 7) ^ g) << 4) + 4u * (uint32_t)(s & 3);
-  const uint32_t d = dst + (s >> 5) * atom + 128u * (uint32_t)g + col;
-  const int w = m.slot_width[s];
-  const uint32_t src = codes + m.slot_koff[s] + 2u * (uint32_t)(w * g);
-  const uint32_t sn = norms + 128u * m.slot_group[s] + 16u * (uint32_t)g;
-  const bool split = s < n_split;
-  const uint32_t dl = dst_lo + (uint32_t)(s >> 2) * 128 + 16u * (uint32_t)g + 4u * (uint32_t)(s & 3);
-  switch (w) {
-    case 1: key_slot<1>(src, sn, tab, lane4, d, split, dl, lo_rows); break;
-    case 2: key_slot<2>(src, sn, tab, lane4, d, split, dl, lo_rows); break;
-    case 3: key_slot<3>(src, sn, tab, lane4, d, split, dl, lo_rows); break;
-    case 4: key_slot<4>(src, sn, tab, lane4, d, split, dl, lo_rows); break;
-    case 5: key_slot<5>(src, sn, tab, lane4, d, split, dl, lo_rows); break;
-    case 6: key_slot<6>(src, sn, tab, lane4, d, split, dl, lo_rows); break;
-    case 7: key_slot<7>(src, sn, tab, lane4, d, split, dl, lo_rows); break;
-    case 8: key_slot<8>(src, sn, tab, lane4, d, split, dl, lo_rows); break;
-    default:  // no code: its query coordinate is 0, but the operand has to be finite
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        sts32(d + 1024 * u, 0);
-        if (split) sts32(dl + lo_rows * u, 0);
-      }
-  }
+  KeyLane k;
+  k.w = m.slot_width[s];
+  k.src = k.w ? m.slot_koff[s] + 2u * (k.w * g) : 0u;
+  k.sn = norms + (k.w ? 128u * m.slot_group[s] : 0u) + 16u * (uint32_t)g;
+  k.col = (s >> 5) * atom + 128u * (uint32_t)g + (uint32_t)((((s >> 2) & 7) ^ g) << 4) + 4u * (uint32_t)(s & 3);
+  return k;
 }
 
-// Norms of a lane's 16 tokens (16 a + 8 b + 2 c + l) as pairs over l, word 2 a + b,
-// divided by 16; tokens from n_tok on count 0.
-__device__ __forceinline__ void value_norms(uint32_t norms, int lane, int n_tok, uint32_t (&n)[8]) {
-  const int c = lane & 3;
-  uint32_t e[4], o[4];
-  asm("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(e[0]), "=r"(e[1]), "=r"(e[2]), "=r"(e[3]) : "r"(norms + 32u * c));
-  asm("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]) : "r"(norms + 32u * c + 16u));
+// Words and norms of a portion as they come from a tile: 2 words from the one that
+// its first byte lies in for widths up to 4, 5 for any (the words behind a portion
+// are inside the tile).
+struct KeyRaw {
+  uint32_t x[5];
+  uint4 n;
+};
+template <int NW>
+__device__ __forceinline__ void load_keys(KeyRaw& r, const uint8_t* tile, const KeyLane& k) {
+  const uint32_t* p = reinterpret_cast<const uint32_t*>(tile + (k.src & ~3u));
+#pragma unroll
+  for (int i = 0; i < NW; ++i) r.x[i] = ldg32(p + i);
+  r.n = ldg128(tile + k.sn);
+}
+
+// Widths up to 4, no low parts: a portion's 8 pairs are 2 w bits each, at most 64 bits.  dst: the
+// operand's row of the tile's first token.
+__device__ __forceinline__ void keys_by_pair(const KeyLane& k, const KeyRaw& r, uint32_t tab,
+                                             uint32_t lane4, uint32_t dst) {
+  const uint32_t w2 = 2 * k.w, odd = (k.src & 2u) * 8u, mask = (1u << w2) - 1;
+  uint32_t x0 = __funnelshift_r(r.x[0], r.x[1], odd), x1 = r.x[1] >> odd;
+  // lookup address = base + index * step
+  const uint32_t step = k.w == 4 ? 4u : 128u;
+  uint32_t base = tab + kDqZero;
+  base = k.w == 1 ? tab + kDqPairs + (kTabP32W1 - kTabP32W3) + lane4 : base;
+  base = k.w == 2 ? tab + kDqPairs + (kTabP32W2 - kTabP32W3) + lane4 : base;
+  base = k.w == 3 ? tab + kDqPairs + lane4 : base;
+  base = k.w == 4 ? tab + kDqPair4 : base;
+  const uint32_t d = dst + k.col;
+  uint32_t v[8];
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
-    uint32_t v = __byte_perm(e[u >> 1], o[u >> 1], (u & 1) ? 0x7632 : 0x5410);
-    if (n_tok < 64) {
-      const int t = 8 * u + 2 * c;
-      if (t >= n_tok) v = 0;
-      else if (t + 1 >= n_tok) v &= 0xffffu;
-    }
-    n[u] = h2mul(v, 0x2c002c00u);  // 1 / 16
+    v[u] = lds32((x0 & mask) * step + base);
+    x0 = __funnelshift_r(x0, x1, w2);
+    x1 >>= w2;
+  }
+  const uint32_t nw[4] = {r.n.x, r.n.y, r.n.z, r.n.w};
+#pragma unroll
+  for (int u = 0; u < 8; u += 2) {
+    const __half2 n = __hmul2(as_h2(nw[u >> 1]), __float2half2_rn(0.125f));
+    sts32(d + 1024 * u, as_u32(__hmul2(as_h2(v[u]), __low2half2(n))));
+    sts32(d + 1024 * (u + 1), as_u32(__hmul2(as_h2(v[u + 1]), __high2half2(n))));
   }
 }
 
-template <int W, int I>
-__device__ __forceinline__ void value_pairs(const uint32_t* x, const uint32_t (&n)[8], uint32_t tab,
-                                            uint32_t lane4, uint32_t dst, uint32_t g16) {
-  // pair I: codes 2 I, 2 I + 1 = tokens l = 0, 1 of (a, b, h) = (I / 4, I / 2 % 2, I % 2)
-  constexpr int u = I >> 1, h = I & 1;
-  const uint32_t v = h2mul(code_pair_hi<W, I>(x, tab, lane4), n[u]);
-  sts32(dst + 1024 * h + ((16u * u) ^ g16), v);
-  if constexpr (I < 15) value_pairs<W, I + 1>(x, n, tab, lane4, dst, g16);
+// Any width, code by code.  With `low`, the rests of the products beyond fp16 go to dl, the lane's
+// place among core matrices of 8 rows x 16 bytes (lo_rows bytes from one 8 tokens to the next).
+__device__ __forceinline__ void keys_by_code(const KeyLane& k, const KeyRaw& r, uint32_t tab,
+                                             uint32_t dst, bool low, uint32_t dl, uint32_t lo_rows) {
+  const uint32_t w = k.w, mask = (1u << w) - 1, odd = (k.src & 2u) * 8u;
+  // entries of width w; no code: index 0 of the zero
+  const uint32_t base = tab + (w ? kDqSingles + 2048u - (8u << w) : kDqZero);
+  uint32_t x[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = __funnelshift_r(r.x[i], r.x[i + 1], odd);
+  const uint32_t nw[4] = {r.n.x, r.n.y, r.n.z, r.n.w};
+  const uint32_t d = dst + k.col;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t e0[4], e1[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      e0[u] = lds32((x[0] & mask) * 4 + base);
+      e1[u] = lds32(((x[0] >> w) & mask) * 4 + base);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) x[i] = __funnelshift_r(x[i], x[i + 1], 2 * w);
+      x[3] >>= 2 * w;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const __half2 hi = as_h2(__byte_perm(e0[u], e1[u], 0x5410)), lo = as_h2(__byte_perm(e0[u], e1[u], 0x7632));
+      const __half2 n = __hmul2(as_h2(nw[2 * half + (u >> 1)]), __float2half2_rn(0.125f));
+      const __half2 nn = (u & 1) ? __high2half2(n) : __low2half2(n);
+      const __half2 p = __hmul2(hi, nn);
+      sts32(d + 4096 * half + 1024 * u, as_u32(p));
+      // hi * n - fp16(hi * n) is exact in one fma (above the subnormals); lo * n joins it
+      if (low)
+        sts32(dl + (4 * half + u) * lo_rows, as_u32(__hfma2(lo, nn, __hfma2(hi, nn, __hneg2(p)))));
+    }
+  }
+}
+
+// Value codes of a lane (portion `lane` of 16 dims) and the norms of its 16 tokens
+// 16 a + 8 b + 2 c + l (rows l = 0, 1 of its c).
+// Codes of more than 4 bits are fetched when they are due: holding 8 words a lane ahead
+// costs every width its registers.
+struct ValueRaw {
+  uint32_t x[4];
+  uint4 e, o;
+};
+__device__ __forceinline__ void load_values(ValueRaw& r, const uint8_t* tile, int kb, int vb, int step, int lane) {
+  const uint32_t* p = reinterpret_cast<const uint32_t*>(tile + 1024 * kb + (step * 32 + lane) * 4 * vb);
+  if (vb <= 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < vb) r.x[i] = ldg32(p + i);
+  }
+  const uint4* n = reinterpret_cast<const uint4*>(tile + 1024 * (kb + vb) + 32 * (lane & 3));
+  r.e = ldg128(n);
+  r.o = ldg128(n + 1);
+}
+// The norms as pairs over l, word 2 a + b, divided by 16; tokens from n_tok on count 0.
+__device__ __forceinline__ void value_norms(const ValueRaw& r, int lane, int n_tok, uint32_t (&n)[8]) {
+  const uint32_t e[4] = {r.e.x, r.e.y, r.e.z, r.e.w}, o[4] = {r.o.x, r.o.y, r.o.z, r.o.w};
+#pragma unroll
+  for (int u = 0; u < 8; ++u) n[u] = __byte_perm(e[u >> 1], o[u >> 1], (u & 1) ? 0x7632 : 0x5410);
+  if (n_tok < 64) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int t = 8 * u + 2 * (lane & 3);
+      n[u] = t >= n_tok ? 0u : (t + 1 >= n_tok ? n[u] & 0xffffu : n[u]);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 8; ++u) n[u] = as_u32(__hmul2(as_h2(n[u]), __float2half2_rn(0.0625f)));
+}
+
+// Pair I: codes 2 I, 2 I + 1 = tokens l = 0, 1 of (a, b, h) = (I / 4, I / 2 % 2, I % 2).
+// All lookups of a batch come before its stores: a load may not pass a store whose address
+// the compiler cannot tell apart (one by one measured a third of the rate).
+template <int W, int I, int N>
+__device__ __forceinline__ void value_lookups(const uint32_t* x, uint32_t tab, uint32_t lane4, uint32_t* v) {
+  v[0] = code_pair_hi<W, I>(x, tab, lane4);
+  if constexpr (N > 1) value_lookups<W, I + 1, N - 1>(x, tab, lane4, v + 1);
 }
 
 template <int W>
-__device__ __forceinline__ void value_portion(uint32_t src, const uint32_t (&n)[8], uint32_t tab,
-                                              uint32_t lane4, uint32_t dst, uint32_t g16) {
-  uint32_t x[9];
+__device__ __forceinline__ void value_portion(const ValueRaw& r, const uint32_t* due,
+                                              const uint32_t (&n)[8], uint32_t tab, uint32_t lane4,
+                                              uint32_t dst, uint32_t g16) {
+  uint32_t x[W + 1];
 #pragma unroll
-  for (int i = 0; i < W; ++i) x[i] = lds32(src + 4 * i);
+  for (int i = 0; i < W; ++i) x[i] = W <= 4 ? r.x[i & 3] : ldg32(due + i);
   x[W] = 0;
-  value_pairs<W, 0>(x, n, tab, lane4, dst, g16);
+  uint32_t v[8];
+  value_lookups<W, 0, 8>(x, tab, lane4, v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    sts32(dst + 1024 * (i & 1) + ((16u * (i >> 1)) ^ g16), as_u32(__hmul2(as_h2(v[i]), as_h2(n[i >> 1]))));
+  value_lookups<W, 8, 8>(x, tab, lane4, v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    sts32(dst + 1024 * (i & 1) + ((16u * (4 + (i >> 1))) ^ g16),
+          as_u32(__hmul2(as_h2(v[i]), as_h2(n[4 + (i >> 1)]))));
 }
 
 // 16 dims (16 step .. + 15) of a tile's values into the atom at dst.
-__device__ __forceinline__ void dequant_values(int vb, int step, int lane, uint32_t codes,
-                                               const uint32_t (&n)[8], uint32_t tab, uint32_t dst) {
+__device__ __forceinline__ void dequant_values(const uint8_t* tile, int kb, int vb, int step, int lane,
+                                               const ValueRaw& r, const uint32_t (&n)[8], uint32_t tab,
+                                               uint32_t dst) {
   const uint32_t lane4 = 4u * (uint32_t)lane, g = (uint32_t)lane >> 2, c = (uint32_t)lane & 3;
-  const uint32_t src = codes + (uint32_t)(step * 32 + lane) * 4u * (uint32_t)vb;
   const uint32_t d = dst + (uint32_t)step * 2048 + g * 128 + c * 4;  // dim 16 step + g, + 8: 1024 on
+  const uint32_t* due = reinterpret_cast<const uint32_t*>(tile + 1024 * kb + (step * 32 + lane) * 4 * vb);
   switch (vb) {
-    case 1: value_portion<1>(src, n, tab, lane4, d, g << 4); break;
-    case 2: value_portion<2>(src, n, tab, lane4, d, g << 4); break;
-    case 3: value_portion<3>(src, n, tab, lane4, d, g << 4); break;
-    case 4: value_portion<4>(src, n, tab, lane4, d, g << 4); break;
-    case 5: value_portion<5>(src, n, tab, lane4, d, g << 4); break;
-    case 6: value_portion<6>(src, n, tab, lane4, d, g << 4); break;
-    case 7: value_portion<7>(src, n, tab, lane4, d, g << 4); break;
-    default: value_portion<8>(src, n, tab, lane4, d, g << 4); break;
+    case 1: value_portion<1>(r, due, n, tab, lane4, d, g << 4); break;
+    case 2: value_portion<2>(r, due, n, tab, lane4, d, g << 4); break;
+    case 3: value_portion<3>(r, due, n, tab, lane4, d, g << 4); break;
+    case 4: value_portion<4>(r, due, n, tab, lane4, d, g << 4); break;
+    case 5: value_portion<5>(r, due, n, tab, lane4, d, g << 4); break;
+    case 6: value_portion<6>(r, due, n, tab, lane4, d, g << 4); break;
+    case 7: value_portion<7>(r, due, n, tab, lane4, d, g << 4); break;
+    default: value_portion<8>(r, due, n, tab, lane4, d, g << 4); break;
   }
 }
 
