@@ -13,10 +13,10 @@
 //     2^8: then the row's output in tensor memory is rescaled (by its own threads,
 //     while no product on it runs).
 //     The first warp of each group of four also issues the group's products, as soon as the
-//     group has written its P: one hand-off less than a warp of its own, and 16 warps leave
-//     128 registers each (a 17th costs a quarter of them, and spills in the loop).
+//     group has written its P: one hand-off less than a warp of its own.
 //   * warps 8-15       tiles of codes to operands (gtq_dequant.cuh): keys run two tiles ahead
-//     of values, and a warp's loads of the one are in flight while it works on the other
+//     of values, and a warp's loads of the one are in flight while it works on the other.
+//     (24 warps, 16 of them here, measured 1.4 times slower: at 80 registers the loops spill.)
 // With 129 rows or more (NQ = 2) the two softmax groups take 128 rows each: while
 // one group's products run, the other computes.  With fewer (NQ = 1) they share
 // the rows and take the token blocks in turns, each with an output of its own;
@@ -42,6 +42,7 @@ constexpr int kSoftWarps = 8;
 constexpr int kDqWarps = 8;
 constexpr int kChunkThreads = 32 * (kSoftWarps + kDqWarps);
 constexpr int kBlockTok = 128;     // tokens of a step
+constexpr int kAhead = 6;          // packed tiles between a prefetch and its use
 constexpr int kSplitSlots = 8;     // slots (pairs of coordinates) with a low part
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescale = 8.f;    // growth of the maximum (log2) that moves the reference
@@ -126,50 +127,79 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   return r;
 }
 
-// Probabilities of one row's 128 scores at tensor-memory column `s`, written back as fp16;
-// cnt of them count.  Returns their sum; `mx` (-inf if none counts) has been found before.
+// two fp32 additions in one instruction
+__device__ __forceinline__ uint64_t pack_f2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack_f2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Maximum of one row's first cnt of 128 scores at tensor-memory column `s`.
 template <bool MASK>
 __device__ __forceinline__ float row_max(uint32_t s, int cnt) {
-  float mx = -INFINITY;
-#pragma unroll 2
+  float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     uint32_t r[32];
     tc_ld32(s + 32 * c, r);
     tc_wait_ld();
-    float m0 = -INFINITY, m1 = -INFINITY;
+    const int left = cnt - 32 * c;
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-      const float a = __uint_as_float(r[e]), b = __uint_as_float(r[e + 1]);
-      m0 = fmaxf(m0, !MASK || 32 * c + e < cnt ? a : -INFINITY);
-      m1 = fmaxf(m1, !MASK || 32 * c + e + 1 < cnt ? b : -INFINITY);
+    for (int e = 0; e < 32; e += 4) {
+      float x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = !MASK || e + i < left ? __uint_as_float(r[e + i]) : -INFINITY;
+      m0 = max3(m0, x[0], x[1]);
+      m1 = max3(m1, x[2], x[3]);
     }
-    mx = fmaxf(mx, fmaxf(m0, m1));
   }
-  return mx;
+  return fmaxf(m0, m1);
 }
+// Probabilities 2^(score - ref), written back over the scores as fp16 (128 scores become 64
+// columns); returns their sum, taken before they are rounded.
 template <bool MASK>
 __device__ __forceinline__ float row_exp(uint32_t s, int cnt, float ref) {
-  float s0 = 0.f, s1 = 0.f;
-#pragma unroll 2
+  const uint64_t neg = pack_f2(-ref, -ref);
+  uint64_t s0 = 0, s1 = 0;
+#pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     uint32_t r[32], p[16];
     tc_ld32(s + 32 * c, r);
     tc_wait_ld();
+    const int left = cnt - 32 * c;
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
-      float a = ex2(__uint_as_float(r[e]) - ref), b = ex2(__uint_as_float(r[e + 1]) - ref);
+      float x, y;
+      unpack_f2(add_f2(pack_f2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), neg), x, y);
+      x = ex2(x);
+      y = ex2(y);
       if (MASK) {
-        a = 32 * c + e < cnt ? a : 0.f;
-        b = 32 * c + e + 1 < cnt ? b : 0.f;
+        x = e < left ? x : 0.f;
+        y = e + 1 < left ? y : 0.f;
       }
-      s0 += a;
-      s1 += b;
-      p[e / 2] = pack_h2(a, b);
+      uint64_t& sum = (e & 2) ? s1 : s0;
+      sum = add_f2(sum, pack_f2(x, y));
+      p[e / 2] = pack_h2(x, y);
     }
     tc_st16(s + 16 * c, p);
   }
   tc_wait_st();
-  return s0 + s1;
+  float x, y;
+  unpack_f2(add_f2(s0, s1), x, y);
+  return x + y;
 }
 
 template <int NQ>
@@ -242,10 +272,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ms.tmem, 0);  // the same in all lanes, and known to be
-  // log2(e) / (sqrt(d) sqrt(m)) and the keys' factor 1 / 8 undone
+  // log2(e) / (sqrt(d) sqrt(m)) and the keys' factor 1 / 16 undone
   if (tid < kD)
     ms.qscale[tid] = (tid >> 1) < ms.m.n_slots
-                         ? 8.f * kLog2e * 0.08838834764831845f * ms.m.inv_sqrt_m[ms.m.slot_group[tid >> 1]]
+                         ? 16.f * kLog2e * 0.08838834764831845f * ms.m.inv_sqrt_m[ms.m.slot_group[tid >> 1]]
                          : 0.f;
   __syncthreads();
   int failed = 0;
@@ -527,10 +557,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     const uint32_t tab = sb + M::tab;
     // quads dw and 15 - dw of the keys, dims 16 dw .. of the values, of every tile
     const uint32_t norms = key_norm_offset(a.kb, a.vb);
-    const KeyLane k0 = key_lane(ms.m, dw, lane, 16384, norms), k1 = key_lane(ms.m, 15 - dw, lane, 16384, norms);
+    const KeyLane k0 = key_lane(ms.m, dw, lane, 16384, norms, tab);
+    const KeyLane k1 = key_lane(ms.m, 15 - dw, lane, 16384, norms, tab);
     const bool low = dw < kSplitSlots / 4;  // slots of quad dw leave low parts
-    const uint32_t lo_lane = (uint32_t)dw * 128 + 16u * (lane & 7) + 4u * (lane >> 3);
     const bool code0 = low || __any_sync(0xffffffffu, k0.w > 4), code1 = __any_sync(0xffffffffu, k1.w > 4);
+    const uint32_t lo_lane = (uint32_t)dw * 128 + 16u * (lane & 7) + 4u * (lane >> 3);
     // tile addresses: page numbers are read a tile ahead of their use
     const int64_t t0 = s0 / kTile;
     const uint8_t* const base = a.packed + (a.sm.table ? (int64_t)h * a.sm.tile_bytes
@@ -552,9 +583,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     auto put_keys = [&](int t, const uint8_t* p) {
       const uint32_t dst = sb + M::k + ((t >> 1) & 1) * kKBuf, row = dst + (t & 1) * 8192;
       if (code0) keys_by_code(k0, r0, tab, row, low, dst + 32768 + (t & 1) * 2048 + lo_lane, 256);
-      else keys_by_pair(k0, r0, tab, 4u * lane, row);
+      else keys_by_pair(k0, r0, row);
       if (!code1) {
-        keys_by_pair(k1, r1, tab, 4u * lane, row);
+        keys_by_pair(k1, r1, row);
       } else {  // widths above 4 beyond the first half of the slots: fetched when they are due
         KeyRaw r;
         load_keys<5>(r, p, k1);
@@ -587,6 +618,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       // the next tile's keys, in flight during the values
       const uint8_t* next = t + 1 < nt ? tile_at(t + 1) : nullptr;
       if (next) fetch_keys(next);
+      // and what is due three steps on, towards the L2 cache (an eighth of the tile's lines a warp)
+      if (t + kAhead < nt && lane * 1024 < (int)a.sm.tile_bytes) {
+        const uint8_t* p = base + (pages ? (int64_t)__ldg(pages + t + kAhead) * a.sm.hkv : (int64_t)(t + kAhead)) * a.sm.tile_bytes;
+        if (lane * 1024 + dw * 128 < (int)a.sm.tile_bytes)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(p + lane * 1024 + dw * 128));
+      }
       if (v >= 0) {
         const int j = v >> 1;
         if (!(v & 1) && j >= 2 && !mbar_wait(bar(kVEmpty + (j & 1)), ((j >> 1) & 1) ^ 1)) { failed = 1; break; }

@@ -1,21 +1,23 @@
 // Packed tiles to fp16 matrix operands in shared memory, for the tcgen05
 // kernels that attend over the packed cache.
 //
-// Keys, one tile of 64 tokens: rows = tokens, columns = packed coordinates
-// (slot s: columns 2s, 2s + 1), value cb[code] * norm / 8, K-major with the
-// 128-byte swizzle in two atoms of 64 columns.  A lane takes the portion of one
-// slot for tokens g, g + 8, ..., g + 56 (g = lane % 8), a warp four neighbouring
-// slots: with the swizzle its 4-byte stores fall into 32 different banks.
-// Values: rows = rotated dims, columns = the tile's 64 tokens, cb[code] * norm /
-// 16, one swizzled atom; a lane takes a portion (two dims, 16 tokens).
-// Powers of two keep the largest norm (65504) times the largest centroid in the
-// fp16 range; both are undone in the queries and at the end.
+// Eight warps share a tile.  Keys: rows = tokens, columns = packed coordinates
+// (slot s: columns 2s, 2s + 1), K-major with the 128-byte swizzle in two atoms of 64
+// columns; a warp takes four neighbouring slots at a time, a lane one of them for tokens g,
+// g + 8, ..., g + 56 (g = lane % 8): with the swizzle its 4-byte stores fall into 32
+// different banks.  Values: rows = rotated dims, columns = the tile's 64 tokens, one
+// swizzled atom; a warp takes 16 dims, a lane two of them for 16 tokens.
+//
+// An element is cb[code] / 16 * norm: the power of two keeps the largest norm
+// (65504) times the largest centroid in the fp16 range, and is undone in the
+// queries and at the end.
 //
 // Keys of widths up to 4 take a pair of codes in one lookup, every lane by its own
 // width (mask, table, multiplier), so that four slots of different widths run as
-// one instruction stream: straight-line code per width measured 2.5 times slower,
-// waiting for instructions.  Wider codes, and slots that leave a low part, are
-// looked up one by one in a loop.
+// one instruction stream (code per width, one after another for the widths of a
+// warp, measured 1.3 times slower).  Wider codes, and slots that leave a low part, are
+// looked up one by one.  All lookups of a portion come before its stores: a load may
+// not pass a store whose address the compiler cannot tell apart.
 #pragma once
 
 #include "gtq_internal.h"
@@ -23,7 +25,7 @@
 
 namespace gtq {
 
-// Lookup tables in shared memory (fp16 values of the codebook): pair tables of
+// Lookup tables in shared memory (fp16 values of the codebook / 16): pair tables of
 // widths 3, 2, 1 with a copy per lane, as they lie in the decode image (kTabP32W3
 // .. kTabS32W5), a pair table of width 4 in one copy, single codes of all widths
 // (kTabSS: hi | lo << 16), and a zero.
@@ -35,17 +37,22 @@ constexpr uint32_t kDqZero = kDqSingles + 2048u;
 constexpr uint32_t kDqBytes = kDqZero + 128u;
 static_assert(kDqBytes % 128 == 0, "dequantisation tables");
 
+__device__ __forceinline__ __half2 as_h2(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
+__device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
+
 // Copies the tables from the decode image (all threads of the block).
 __device__ __forceinline__ void load_dequant_tables(uint8_t* tab, const uint4* image, int tid,
                                                     int n_threads) {
   const uint8_t* img = reinterpret_cast<const uint8_t*>(image);
   const uint32_t* ss = reinterpret_cast<const uint32_t*>(img + kTabSS);
-  for (int i = tid; i < (int)(kDqPairBytes / 16); i += n_threads)
-    reinterpret_cast<uint4*>(tab + kDqPairs)[i] = reinterpret_cast<const uint4*>(img + kTabP32W3)[i];
-  for (int i = tid; i < 512; i += n_threads) reinterpret_cast<uint32_t*>(tab + kDqSingles)[i] = ss[i];
+  const uint32_t* pp = reinterpret_cast<const uint32_t*>(img + kTabP32W3);
+  auto scaled = [](uint32_t v) { return as_u32(__hmul2(as_h2(v), __float2half2_rn(0.0625f))); };
+  for (int i = tid; i < (int)(kDqPairBytes / 4); i += n_threads)
+    reinterpret_cast<uint32_t*>(tab + kDqPairs)[i] = scaled(pp[i]);
+  for (int i = tid; i < 512; i += n_threads) reinterpret_cast<uint32_t*>(tab + kDqSingles)[i] = scaled(ss[i]);
   for (int i = tid; i < 256; i += n_threads)
     reinterpret_cast<uint32_t*>(tab + kDqPair4)[i] =
-        __byte_perm(ss[kSingleOff(4) / 4 + (i & 15)], ss[kSingleOff(4) / 4 + (i >> 4)], 0x5410);
+        scaled(__byte_perm(ss[kSingleOff(4) / 4 + (i & 15)], ss[kSingleOff(4) / 4 + (i >> 4)], 0x5410));
   if (tid < 32) reinterpret_cast<uint32_t*>(tab + kDqZero)[tid] = 0;
 }
 
@@ -103,24 +110,30 @@ __device__ __forceinline__ uint32_t code_pair_hi(const uint32_t* x, uint32_t tab
     return __byte_perm(single<W, 2 * U>(x, tab), single<W, 2 * U + 1>(x, tab), 0x5410);
 }
 
-__device__ __forceinline__ __half2 as_h2(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
-__device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
-
 // A lane's slot among four (4 quad .. 4 quad + 3) of a tile's keys.
 struct KeyLane {
   uint32_t src;      // byte offset of its portion in the tile
   uint32_t sn;       // of its norms
   uint32_t col;      // of its pair in the operand: row g, swizzled column
   uint32_t w;        // width (0: no code)
+  uint32_t base;     // lookup of a pair (widths up to 4): base + index * step
+  uint32_t step;
 };
 __device__ __forceinline__ KeyLane key_lane(const HeadMeta& m, int quad, int lane, uint32_t atom,
-                                            uint32_t norms) {
+                                            uint32_t norms, uint32_t tab) {
   const int g = lane & 7, s = 4 * quad + (lane >> 3);
+  const uint32_t lane4 = 4u * (uint32_t)lane;
   KeyLane k;
   k.w = m.slot_width[s];
   k.src = k.w ? m.slot_koff[s] + 2u * (k.w * g) : 0u;
   k.sn = norms + (k.w ? 128u * m.slot_group[s] : 0u) + 16u * (uint32_t)g;
   k.col = (s >> 5) * atom + 128u * (uint32_t)g + (uint32_t)((((s >> 2) & 7) ^ g) << 4) + 4u * (uint32_t)(s & 3);
+  k.step = k.w == 4 ? 4u : 128u;
+  k.base = tab + (k.w == 1   ? kDqPairs + (kTabP32W1 - kTabP32W3) + lane4
+                  : k.w == 2 ? kDqPairs + (kTabP32W2 - kTabP32W3) + lane4
+                  : k.w == 3 ? kDqPairs + lane4
+                  : k.w == 4 ? kDqPair4
+                             : kDqZero);
   return k;
 }
 
@@ -133,37 +146,32 @@ struct KeyRaw {
 };
 template <int NW>
 __device__ __forceinline__ void load_keys(KeyRaw& r, const uint8_t* tile, const KeyLane& k) {
-  const uint32_t* p = reinterpret_cast<const uint32_t*>(tile + (k.src & ~3u));
+  const uint8_t* p = tile + (k.src & ~3u);
 #pragma unroll
-  for (int i = 0; i < NW; ++i) r.x[i] = ldg32(p + i);
+  for (int i = 0; i < NW; ++i) r.x[i] = ldg32(p + 4 * i);
   r.n = ldg128(tile + k.sn);
 }
 
-// Widths up to 4, no low parts: a portion's 8 pairs are 2 w bits each, at most 64 bits.  dst: the
-// operand's row of the tile's first token.
-__device__ __forceinline__ void keys_by_pair(const KeyLane& k, const KeyRaw& r, uint32_t tab,
-                                             uint32_t lane4, uint32_t dst) {
+// Widths up to 4, no low parts: four of the portion's 8 pairs are 8 w bits, at most a word.  dst:
+// the operand's row of the tile's first token.
+__device__ __forceinline__ void keys_by_pair(const KeyLane& k, const KeyRaw& r, uint32_t dst) {
   const uint32_t w2 = 2 * k.w, odd = (k.src & 2u) * 8u, mask = (1u << w2) - 1;
-  uint32_t x0 = __funnelshift_r(r.x[0], r.x[1], odd), x1 = r.x[1] >> odd;
-  // lookup address = base + index * step
-  const uint32_t step = k.w == 4 ? 4u : 128u;
-  uint32_t base = tab + kDqZero;
-  base = k.w == 1 ? tab + kDqPairs + (kTabP32W1 - kTabP32W3) + lane4 : base;
-  base = k.w == 2 ? tab + kDqPairs + (kTabP32W2 - kTabP32W3) + lane4 : base;
-  base = k.w == 3 ? tab + kDqPairs + lane4 : base;
-  base = k.w == 4 ? tab + kDqPair4 : base;
-  const uint32_t d = dst + k.col;
+  uint32_t x[2];
+  x[0] = __funnelshift_r(r.x[0], r.x[1], odd);
+  x[1] = __funnelshift_rc(x[0], r.x[1] >> odd, 4 * w2);
   uint32_t v[8];
 #pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    v[u] = lds32((x0 & mask) * step + base);
-    x0 = __funnelshift_r(x0, x1, w2);
-    x1 >>= w2;
-  }
+  for (int u = 0; u < 4; ++u)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      v[4 * i + u] = lds32((x[i] & mask) * k.step + k.base);
+      x[i] >>= w2;
+    }
   const uint32_t nw[4] = {r.n.x, r.n.y, r.n.z, r.n.w};
+  const uint32_t d = dst + k.col;
 #pragma unroll
   for (int u = 0; u < 8; u += 2) {
-    const __half2 n = __hmul2(as_h2(nw[u >> 1]), __float2half2_rn(0.125f));
+    const __half2 n = as_h2(nw[u >> 1]);
     sts32(d + 1024 * u, as_u32(__hmul2(as_h2(v[u]), __low2half2(n))));
     sts32(d + 1024 * (u + 1), as_u32(__hmul2(as_h2(v[u + 1]), __high2half2(n))));
   }
@@ -176,26 +184,33 @@ __device__ __forceinline__ void keys_by_code(const KeyLane& k, const KeyRaw& r, 
   const uint32_t w = k.w, mask = (1u << w) - 1, odd = (k.src & 2u) * 8u;
   // entries of width w; no code: index 0 of the zero
   const uint32_t base = tab + (w ? kDqSingles + 2048u - (8u << w) : kDqZero);
-  uint32_t x[4];
+  uint32_t x[5];
 #pragma unroll
   for (int i = 0; i < 4; ++i) x[i] = __funnelshift_r(r.x[i], r.x[i + 1], odd);
+  x[4] = 0;
   const uint32_t nw[4] = {r.n.x, r.n.y, r.n.z, r.n.w};
   const uint32_t d = dst + k.col;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
+    // four pairs are 8 w bits: the second four start in word w / 4
+    const uint32_t at = 8 * w;
+    const uint32_t a0 = half == 0 ? x[0] : (at >= 64 ? x[2] : (at >= 32 ? x[1] : x[0]));
+    const uint32_t a1 = half == 0 ? x[1] : (at >= 64 ? x[3] : (at >= 32 ? x[2] : x[1]));
+    const uint32_t a2 = half == 0 ? x[2] : (at >= 64 ? x[4] : (at >= 32 ? x[3] : x[2]));
+    uint32_t y0 = half == 0 ? a0 : __funnelshift_r(a0, a1, at & 31u);
+    uint32_t y1 = half == 0 ? a1 : __funnelshift_r(a1, a2, at & 31u);
     uint32_t e0[4], e1[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      e0[u] = lds32((x[0] & mask) * 4 + base);
-      e1[u] = lds32(((x[0] >> w) & mask) * 4 + base);
-#pragma unroll
-      for (int i = 0; i < 3; ++i) x[i] = __funnelshift_r(x[i], x[i + 1], 2 * w);
-      x[3] >>= 2 * w;
+      e0[u] = lds32((y0 & mask) * 4 + base);
+      e1[u] = lds32(((y0 >> w) & mask) * 4 + base);
+      y0 = __funnelshift_r(y0, y1, 2 * w);
+      y1 >>= 2 * w;
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const __half2 hi = as_h2(__byte_perm(e0[u], e1[u], 0x5410)), lo = as_h2(__byte_perm(e0[u], e1[u], 0x7632));
-      const __half2 n = __hmul2(as_h2(nw[2 * half + (u >> 1)]), __float2half2_rn(0.125f));
+      const __half2 n = as_h2(nw[2 * half + (u >> 1)]);
       const __half2 nn = (u & 1) ? __high2half2(n) : __low2half2(n);
       const __half2 p = __hmul2(hi, nn);
       sts32(d + 4096 * half + 1024 * u, as_u32(p));
@@ -225,7 +240,7 @@ __device__ __forceinline__ void load_values(ValueRaw& r, const uint8_t* tile, in
   r.e = ldg128(n);
   r.o = ldg128(n + 1);
 }
-// The norms as pairs over l, word 2 a + b, divided by 16; tokens from n_tok on count 0.
+// The norms as pairs over l, word 2 a + b; tokens from n_tok on count 0.
 __device__ __forceinline__ void value_norms(const ValueRaw& r, int lane, int n_tok, uint32_t (&n)[8]) {
   const uint32_t e[4] = {r.e.x, r.e.y, r.e.z, r.e.w}, o[4] = {r.o.x, r.o.y, r.o.z, r.o.w};
 #pragma unroll
@@ -237,8 +252,6 @@ __device__ __forceinline__ void value_norms(const ValueRaw& r, int lane, int n_t
       n[u] = t >= n_tok ? 0u : (t + 1 >= n_tok ? n[u] & 0xffffu : n[u]);
     }
   }
-#pragma unroll
-  for (int u = 0; u < 8; ++u) n[u] = as_u32(__hmul2(as_h2(n[u]), __float2half2_rn(0.0625f)));
 }
 
 // Pair I: codes 2 I, 2 I + 1 = tokens l = 0, 1 of (a, b, h) = (I / 4, I / 2 % 2, I % 2).
