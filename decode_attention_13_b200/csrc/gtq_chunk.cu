@@ -31,6 +31,7 @@
 // them.
 #include <algorithm>
 
+#include "gtq_attn.cuh"
 #include "gtq_dequant.cuh"
 #include "gtq_internal.h"
 #include "gtq_tc.cuh"
@@ -44,7 +45,6 @@ constexpr int kChunkThreads = 32 * (kSoftWarps + kDqWarps);
 constexpr int kBlockTok = 128;     // tokens of a step
 constexpr int kAhead = 6;          // packed tiles between a prefetch and its use
 constexpr int kSplitSlots = 8;     // slots (pairs of coordinates) with a low part
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescale = 8.f;    // growth of the maximum (log2) that moves the reference
 
 // shared memory, from a 1024-byte boundary
@@ -111,63 +111,6 @@ struct ChunkArgs {
   int* status;
 };
 
-__device__ __forceinline__ int64_t chunk_len(const int32_t* lens, int64_t n, int b) {
-  if (!lens) return n;
-  const int64_t c = lens[b];
-  return c < 0 ? 0 : (c < n ? c : n);
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// two fp32 additions in one instruction
-__device__ __forceinline__ uint64_t pack_f2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpack_f2(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
-// Maximum of one row's first cnt of 128 scores at tensor-memory column `s`.
-template <bool MASK>
-__device__ __forceinline__ float row_max(uint32_t s, int cnt) {
-  float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    uint32_t r[32];
-    tc_ld32(s + 32 * c, r);
-    tc_wait_ld();
-    const int left = cnt - 32 * c;
-#pragma unroll
-    for (int e = 0; e < 32; e += 4) {
-      float x[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = !MASK || e + i < left ? __uint_as_float(r[e + i]) : -INFINITY;
-      m0 = max3(m0, x[0], x[1]);
-      m1 = max3(m1, x[2], x[3]);
-    }
-  }
-  return fmaxf(m0, m1);
-}
 // Probabilities 2^(score - ref), written back over the scores as fp16 (128 scores become 64
 // columns); returns their sum, taken before they are rounded.
 template <bool MASK>
@@ -272,11 +215,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ms.tmem, 0);  // the same in all lanes, and known to be
-  // log2(e) / (sqrt(d) sqrt(m)) and the keys' factor 1 / 16 undone
-  if (tid < kD)
-    ms.qscale[tid] = (tid >> 1) < ms.m.n_slots
-                         ? 16.f * kLog2e * 0.08838834764831845f * ms.m.inv_sqrt_m[ms.m.slot_group[tid >> 1]]
-                         : 0.f;
+  if (tid < kD) ms.qscale[tid] = query_scale(ms.m, tid);
   __syncthreads();
   int failed = 0;
 
@@ -300,10 +239,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       __syncwarp();
     };
     auto group_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(2 + grp) : "memory"); };
-    // products of the group, issued by one lane of its first warp; a descriptor's start moves by
-    // adding to the low word
+    // products of the group, issued by one lane of its first warp
     const uint32_t idc = idesc_f16(128);
-    auto step_of = [](uint32_t ks) { return (uint64_t)(((ks >> 2) * 16384 + (ks & 3) * 32) >> 4); };
     const uint32_t d_s = tmem + 128u * grp, d_o = tmem + 256u + 128u * grp;
     auto rotate = [&](uint32_t x, bool more, bool with_lo) {
       // scores (+)= x . (hi + lo)^T of the image (with_lo), or x . hi^T
@@ -312,12 +249,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       for (int part = 0; part < (with_lo ? 2 : 1); ++part)
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          tc_mma(d_s, dx + step_of(ks), di + step_of(ks) + part * (32768 >> 4), idc, more || (part | ks) != 0);
+          tc_mma(d_s, dx + kstep(ks), di + kstep(ks) + part * (32768 >> 4), idc, more || (part | ks) != 0);
     };
     auto scores = [&](int j) {
       const uint64_t dq = smem_desc(sb + M::qhi + tile * kQHi), dk = smem_desc(sb + M::k + (j & 1) * kKBuf);
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks) tc_mma(d_s, dq + step_of(ks), dk + step_of(ks), idc, ks != 0);
+      for (int ks = 0; ks < 8; ++ks) tc_mma(d_s, dq + kstep(ks), dk + kstep(ks), idc, ks != 0);
       tc_mma(d_s, smem_desc_plain(sb + M::qlo + tile * kQLo, 128, 256), dk, idc, 1);
       tc_mma(d_s, dq, smem_desc_plain(sb + M::k + (j & 1) * kKBuf + 32768, 128, 256), idc, 1);
       tc_commit(bar(kSFull + grp));
@@ -333,12 +270,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     const int first = NQ == 2 ? 0 : grp, stride = NQ == 2 ? 1 : 2;  // the group's steps
     // raw queries -> operand, rotated by the tensor cores, back as scaled hi + lo
     if (NQ == 2 || grp == 0) {
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + b * a.qs[0] + hq * a.qs[1] + tok * a.qs[2]);
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const uint4 v = mine ? src[c] : make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(qhi + (c >> 3) * 16384 + (((c & 7) ^ sw) << 4)) = v;
-      }
+      put_query_row(sm + M::qhi + tile * kQHi, lrow,
+                    reinterpret_cast<const uint4*>(a.q + b * a.qs[0] + hq * a.qs[1] + tok * a.qs[2]), mine);
       fence_async();
       group_sync();
       if (issuer) {
@@ -360,22 +293,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         tc_wait_ld();
 #pragma unroll
         for (int k = 0; k < 4; ++k) {  // 8 coordinates each
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int p = 32 * c + 8 * k + 2 * e;
-            float x = __uint_as_float(r[8 * k + 2 * e]) * ms.qscale[p];
-            float y = __uint_as_float(r[8 * k + 2 * e + 1]) * ms.qscale[p + 1];
-            x = fminf(fmaxf(x, -65504.f), 65504.f);
-            y = fminf(fmaxf(y, -65504.f), 65504.f);
-            hi[e] = pack_h2(x, y);
-            const __half2 hh = *reinterpret_cast<__half2*>(&hi[e]);
-            lo[e] = pack_h2(x - __low2float(hh), y - __high2float(hh));
-          }
           const int ch = 4 * c + k;
-          *reinterpret_cast<uint4*>(qhi + (ch >> 3) * 16384 + (((ch & 7) ^ sw) << 4)) =
-              make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          if (ch < 2) *reinterpret_cast<uint4*>(qlo + ch * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          uint4 hi, lo;
+          split8(r + 8 * k, ms.qscale + 8 * ch, hi, lo);
+          *reinterpret_cast<uint4*>(qhi + (ch >> 3) * 16384 + (((ch & 7) ^ sw) << 4)) = hi;
+          if (ch < 2) *reinterpret_cast<uint4*>(qlo + ch * 128) = lo;
         }
       }
       tc_fence_before();

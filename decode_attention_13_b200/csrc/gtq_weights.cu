@@ -1,255 +1,488 @@
 // Attention weights that a chunk gives every cached token (include/gtq.h,
-// gtq_attn_weights).
+// gtq_attn_weights): w_t += sum over rows r of exp(s_rt) / sum_t' exp(s_rt').
+//
+// Two passes over the keys, since a row's sum has to be known before any of its
+// weights: pass 0 leaves every row's maximum and sum (one pair per stretch of
+// tokens), pass 1 the sums over rows.  Each pass is a kernel like the chunk's
+// (gtq_chunk.cu): a block takes up to 128 rows of one KV head and a stretch of its
+// tokens, eight warps turn codes into fp16 operands, scores are tcgen05.mma
+// products into tensor memory, and two groups of four warps read them in turns.
+// Pass 0 has rows on the lanes (a thread keeps one row's maximum and sum); pass 1
+// swaps the operands, so that tokens are on the lanes and a thread adds one token's
+// weights over the rows, in order: no atomics, the same bits every time.
+//
+// The result is fp32, so scores are q (hi + lo) . k (hi + lo) without lo . lo: three
+// products of fp16 halves carry about 22 bits of each factor.
+//
+// Rows beyond 128 of a KV head are more blocks, whose sums lie side by side in the
+// workspace until add_kernel joins them in order.
 #include <algorithm>
 
+#include "gtq_attn.cuh"
+#include "gtq_dequant.cuh"
 #include "gtq_internal.h"
-#include "gtq_unpack.cuh"
+#include "gtq_tc.cuh"
 
 namespace gtq {
 namespace {
 
-constexpr int kRows = 16;       // rows of a block
-constexpr int kThreadsC = 256;
-constexpr float kScale = 0.08838834764831845f;  // 1 / sqrt(128)
+constexpr int kReadWarps = 8;
+constexpr int kDqWarps = 8;
+constexpr int kThreadsW = 32 * (kReadWarps + kDqWarps);
+constexpr int kStepTok = 128;
+constexpr int kRowsW = 128;
+constexpr int kAheadW = 6;  // packed tiles between a prefetch and its use
 
-struct ChunkArgs {
+// shared memory: queries and two steps of keys, each fp16 hi and lo (two swizzled atoms a part)
+constexpr uint32_t kPart = 32768;
+constexpr uint32_t kOffQ = 0;
+constexpr uint32_t kOffK = 2 * kPart;
+constexpr uint32_t kOffTab = kOffK + 4 * kPart;
+constexpr uint32_t kOffMisc = kOffTab + kDqBytes;
+constexpr uint32_t kImageBytes = 65536;  // the keys' rotation, under the keys until the queries are turned
+struct MiscW {
+  alignas(16) HeadMeta m;
+  alignas(16) float qscale[kD];
+  alignas(16) float2 stat[kRowsW];  // pass 0: the second group's rows; pass 1: maximum, 1 / sum
+  int end[kRowsW];                  // pass 1: tokens of the stretch that a row sees
+  uint64_t bar[12];
+  uint32_t tmem;
+};
+constexpr uint32_t kSmemW = kOffMisc + (uint32_t)sizeof(MiscW);
+static_assert(kSmemW <= 232448, "shared memory of a block");
+
+constexpr int kKFull = 0;   // [2] keys of a step written
+constexpr int kKEmpty = 2;  // [2] their products done
+constexpr int kSFull = 4;   // [2] scores written
+constexpr int kImg = 6;
+constexpr int kQRot = 7;
+constexpr int kQFull = 8;
+constexpr int kDrain = 9;   // [2]
+
+struct WeightArgs {
   const uint8_t* packed;
   SeqMap sm;
   int64_t T;
   const __half* q;
   int64_t qs[3];
-  __half* out;
-  int64_t os[3];
   int64_t n;
   const int32_t* chunk_lens;
-  int causal;
-  int gq, hkv, kb, vb;
+  int causal, gq, hkv, kb, vb;
   const HeadMeta* meta;
-  const float* mrow;
-  const float* rv;
-  const uint8_t* singles;  // centroids as fp16 hi | lo (kTabSS of the decode image)
+  const uint8_t* bimg_k;
+  const uint4* dec_image;
   const float* w_in;
   float* w_out;
   int64_t ws[2];
-  float2* stats;           // [heads][rows]: maximum and sum of a row's softmax
+  int row_tiles, splits, n_heads;
+  int64_t span, rows_pad;
+  float2* part_ml;  // [heads][splits][rows_pad]
+  float* part_w;    // [row tiles][heads][T], when there are several row tiles
+  int* status;
 };
 
-struct Shared {
-  HeadMeta m;
-  float cb[kLutEntries + 2];
-  float q[kRows][kD];
-  float k[kTile][kD + 1];
-  float v[kTile][kD];
-  float s[kRows][kTile + 1];
-  float o[kRows][kD];
-  float mx[kRows], sum[kRows], fac[kRows];
-};
-
-__device__ int64_t chunk_len(const ChunkArgs& a, int b) {
-  if (!a.chunk_lens) return a.n;
-  const int64_t c = a.chunk_lens[b];
-  return c < 0 ? 0 : (c < a.n ? c : a.n);
-}
-
-__device__ void load_head(const ChunkArgs& a, int head, Shared& sh) {
-  for (int i = threadIdx.x; i < (int)(sizeof(HeadMeta) / 4); i += kThreadsC)
-    reinterpret_cast<uint32_t*>(&sh.m)[i] = reinterpret_cast<const uint32_t*>(a.meta + head)[i];
-  for (int w = 1; w <= 8; ++w)
-    for (int i = threadIdx.x; i < (1 << w); i += kThreadsC) {
-      const __half2 e = *reinterpret_cast<const __half2*>(a.singles + kSingleOff(w) + 4 * i);
-      sh.cb[lut_base(w) + i] = __half2float(__low2half(e)) + __half2float(__high2half(e));
-    }
-  __syncthreads();
-}
-
-// rows [r0, r0 + kRows) of the head's queries in the keys' rotated bases
-__device__ void load_q(const ChunkArgs& a, int b, int h, int head, int64_t r0, int64_t n_rows, Shared& sh) {
-  for (int i = threadIdx.x; i < kRows * kD; i += kThreadsC) {
-    const int r = i / kD, pos = i % kD;
-    const int64_t row = r0 + r;
-    float x = 0.f;
-    if (row < n_rows) {
-      const int64_t tok = row / a.gq;
-      const __half* q = a.q + b * a.qs[0] + (h * a.gq + row % a.gq) * a.qs[1] + tok * a.qs[2];
-      const float* mr = a.mrow + ((size_t)head * kD + pos) * kD;
-      for (int d = 0; d < kD; ++d) x = fmaf(mr[d], __half2float(q[d]), x);
-    }
-    sh.q[r][pos] = x * kScale;
-  }
-  __syncthreads();
-}
-
-__device__ void load_tile(const ChunkArgs& a, int head, int64_t t, Shared& sh, bool values) {
-  const uint8_t* tile = a.sm.tile(const_cast<uint8_t*>(a.packed), head, t);
-  const int kn = key_norm_offset(a.kb, a.vb);
-  for (int i = threadIdx.x; i < kTile * kD; i += kThreadsC) {
-    const int j = i / kD, p = i % kD;
-    float k = 0.f;
-    const int w = (p >> 1) < sh.m.n_slots ? sh.m.slot_width[p >> 1] : 0;
-    if (w) {
-      const int g = sh.m.slot_group[p >> 1];
-      k = sh.cb[lut_base(w) + key_code(tile, sh.m, j, p, w)] * tile_norm(tile, kn + 128 * g, j) *
-          sh.m.inv_sqrt_m[g];
-    }
-    sh.k[j][p] = k;
-    if (values)
-      sh.v[j][p] = sh.cb[lut_base(a.vb) + value_code(tile, a.kb, a.vb, j, p)] *
-                   tile_norm(tile, value_norm_offset(a.kb, a.vb), j) * kScale;
-  }
-  __syncthreads();
-}
-
-// scores of the rows on the tile in sh.k; -inf where a row sees nothing
-__device__ void score_tile(const ChunkArgs& a, int64_t t, int64_t r0, int64_t n_rows, int64_t len,
-                           int64_t cl, Shared& sh) {
-  for (int i = threadIdx.x; i < kRows * kTile; i += kThreadsC) {
-    const int r = i / kTile, j = i % kTile;
-    float s = 0.f;
-    for (int p = 0; p < kD; ++p) s = fmaf(sh.q[r][p], sh.k[j][p], s);
-    const int64_t tok = t * kTile + j;
-    const int64_t last = a.causal ? len - cl + (r0 + r) / a.gq : len - 1;
-    sh.s[r][j] = r0 + r < n_rows && tok < len && tok <= last ? s : -INFINITY;
-  }
-  __syncthreads();
-}
-
-template <bool WEIGHTS>
-__global__ void __launch_bounds__(kThreadsC) chunk_kernel(ChunkArgs a) {
-  extern __shared__ __align__(16) uint8_t raw[];
-  Shared& sh = *reinterpret_cast<Shared*>(raw);
-  const int head = blockIdx.y, b = head / a.hkv, h = head % a.hkv, tid = threadIdx.x;
-  const int64_t len = a.sm.len(b, a.T), cl = chunk_len(a, b), n_rows = cl * a.gq;
-  const int64_t r0 = (int64_t)blockIdx.x * kRows;
-  if (r0 >= n_rows) return;
-  load_head(a, head, sh);
-  load_q(a, b, h, head, r0, n_rows, sh);
-  for (int i = tid; i < kRows * kD; i += kThreadsC) sh.o[i / kD][i % kD] = 0.f;
-  if (tid < kRows) {
-    sh.mx[tid] = -INFINITY;
-    sh.sum[tid] = 0.f;
-  }
-  for (int64_t t = 0; t * kTile < len; ++t) {
-    load_tile(a, head, t, sh, !WEIGHTS);
-    score_tile(a, t, r0, n_rows, len, cl, sh);
-    if (tid < kRows) {
-      float mx = sh.mx[tid];
-      for (int j = 0; j < kTile; ++j) mx = fmaxf(mx, sh.s[tid][j]);
-      const float ref = mx == -INFINITY ? 0.f : mx;
-      const float fac = expf(sh.mx[tid] - ref);
-      float sum = 0.f;  // a tile's own first: a long row's sum loses less that way
-      for (int j = 0; j < kTile; ++j) {
-        const float p = expf(sh.s[tid][j] - ref);
-        sh.s[tid][j] = p;
-        sum += p;
-      }
-      sh.mx[tid] = mx;
-      sh.sum[tid] = sh.sum[tid] * fac + sum;
-      sh.fac[tid] = fac;
-    }
-    __syncthreads();
-    if (!WEIGHTS)
-      for (int i = tid; i < kRows * kD; i += kThreadsC) {
-        const int r = i / kD, d = i % kD;
-        float o = sh.o[r][d] * sh.fac[r];
-        for (int j = 0; j < kTile; ++j) o = fmaf(sh.s[r][j], sh.v[j][d], o);
-        sh.o[r][d] = o;
-      }
-    __syncthreads();
-  }
-  __syncthreads();
-  if (WEIGHTS) {
-    if (tid < kRows && r0 + tid < n_rows)
-      a.stats[(size_t)head * a.n * a.gq + r0 + tid] = make_float2(sh.mx[tid], sh.sum[tid]);
+template <int PASS>
+__global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_constant__ WeightArgs a) {
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const uint32_t sb = su32(sm);
+  if (sb & 1023u) {  // the swizzled operands need it
+    if (threadIdx.x == 0) atomicOr(a.status, kStatusLayout);
     return;
   }
-  for (int i = tid; i < kRows * kD; i += kThreadsC) {
-    const int r = i / kD, d = i % kD;
-    const int64_t row = r0 + r;
-    if (row >= n_rows) continue;
-    float o = 0.f;
-    for (int p = 0; p < kD; ++p) o = fmaf(sh.o[r][p], a.rv[p * kD + d], o);
-    o = sh.sum[r] > 0.f ? o / sh.sum[r] : 0.f;
-    a.out[b * a.os[0] + (h * a.gq + row % a.gq) * a.os[1] + row / a.gq * a.os[2] + d] = __float2half_rn(o);
+  MiscW& ms = *reinterpret_cast<MiscW*>(sm + kOffMisc);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int head = blockIdx.y, b = head / a.hkv, h = head % a.hkv;
+  const int rt = blockIdx.x % a.row_tiles, sp = blockIdx.x / a.row_tiles;
+  const int64_t len = a.sm.len(b, a.T), cl = chunk_len(a.chunk_lens, a.n, b), n_rows = cl * a.gq;
+  const int64_t r0 = (int64_t)rt * kRowsW, s0 = sp * a.span;
+  const int rows = (int)(n_rows - r0 < 0 ? 0 : (n_rows - r0 < kRowsW ? n_rows - r0 : kRowsW));
+  int64_t seen = len;
+  if (PASS == 0 && a.causal && rows) seen = len - cl + (r0 + rows - 1) / a.gq + 1;
+  const int64_t s1 = seen < s0 + a.span ? seen : s0 + a.span;
+  float2* ml = a.part_ml + ((int64_t)head * a.splits + sp) * a.rows_pad + r0;
+  float* out = nullptr;
+  const float* in = nullptr;
+  if (PASS == 1) {
+    const int64_t at = b * a.ws[0] + h * a.ws[1];
+    if (a.row_tiles == 1) {
+      out = a.w_out + at;
+      in = a.w_in ? a.w_in + at : nullptr;
+    } else {
+      out = a.part_w + ((int64_t)rt * a.n_heads + head) * a.T;
+    }
   }
-}
+  if (rows == 0 || s0 >= s1) {
+    if (PASS == 0) {
+      for (int r = tid; r < rows; r += kThreadsW) ml[r] = make_float2(-INFINITY, 0.f);
+    } else if (a.row_tiles == 1) {  // no row: what was there stays
+      for (int64_t t = s0 + tid; t < s1; t += kThreadsW) out[t] = in ? in[t] : 0.f;
+    }
+    return;
+  }
+  const int nb = (int)((s1 - s0 + kStepTok - 1) / kStepTok), nt = (int)((s1 - s0 + kTile - 1) / kTile);
+  const uint32_t bar0 = su32(ms.bar);
+  auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
 
-__global__ void __launch_bounds__(kThreadsC) weights_kernel(ChunkArgs a) {
-  extern __shared__ __align__(16) uint8_t raw[];
-  Shared& sh = *reinterpret_cast<Shared*>(raw);
-  const int head = blockIdx.y, b = head / a.hkv, h = head % a.hkv, tid = threadIdx.x;
-  const int64_t len = a.sm.len(b, a.T), cl = chunk_len(a, b), n_rows = cl * a.gq;
-  const int64_t t = blockIdx.x;
-  if (t * kTile >= len) return;
-  load_head(a, head, sh);
-  load_tile(a, head, t, sh, false);
-  float w = 0.f;
-  for (int64_t r0 = 0; r0 < n_rows; r0 += kRows) {
-    __syncthreads();
-    load_q(a, b, h, head, r0, n_rows, sh);
-    score_tile(a, t, r0, n_rows, len, cl, sh);
-    if (tid < kTile)
-      for (int r = 0; r < kRows && r0 + r < n_rows; ++r) {
-        const float2 st = a.stats[(size_t)head * a.n * a.gq + r0 + r];
-        if (st.y > 0.f) w += expf(sh.s[r][tid] - st.x) / st.y;
+  // ---------------------------------------------------------------- set-up
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kKFull + i), kDqWarps);
+      mbar_init(bar(kKEmpty + i), 1);
+      mbar_init(bar(kSFull + i), 1);
+      mbar_init(bar(kDrain + i), 1);
+    }
+    mbar_init(bar(kImg), 1);
+    mbar_init(bar(kQRot), 1);
+    mbar_init(bar(kQFull), 4);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    mbar_expect_tx(bar(kImg), kImageBytes);
+    bulk_load(sb + kOffK, a.bimg_k + (size_t)head * kImageBytes, kImageBytes, bar(kImg));
+  }
+  for (int i = tid; i < (int)(sizeof(HeadMeta) / 4); i += kThreadsW)
+    reinterpret_cast<uint32_t*>(&ms.m)[i] = reinterpret_cast<const uint32_t*>(a.meta + head)[i];
+  load_dequant_tables(sm + kOffTab, a.dec_image, tid, kThreadsW);
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(su32(&ms.tmem)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  if (PASS == 1 && tid >= kThreadsW - kRowsW) {  // every row's softmax, from its stretches
+    const int r = tid - (kThreadsW - kRowsW);
+    float top = -INFINITY, total = 0.f;
+    if (r < rows) {
+      const float2* p = a.part_ml + (int64_t)head * a.splits * a.rows_pad + r0 + r;
+      for (int s = 0; s < a.splits; ++s) top = fmaxf(top, p[s * a.rows_pad].x);
+      if (top != -INFINITY)
+        for (int s = 0; s < a.splits; ++s) {
+          const float2 v = p[s * a.rows_pad];
+          total += v.y * ex2(v.x - top);
+        }
+    }
+    ms.stat[r] = total > 0.f ? make_float2(top, 1.f / total) : make_float2(0.f, 0.f);
+    const int64_t end = (a.causal ? len - cl + (r0 + r) / a.gq + 1 : len) - s0;
+    ms.end[r] = r >= rows || end < 0 ? 0 : (end < a.span ? (int)end : (int)a.span);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ms.tmem, 0);
+  if (tid < kD) ms.qscale[tid] = query_scale(ms.m, tid);
+  __syncthreads();
+  int failed = 0;
+
+  if (warp < kReadWarps) {
+    // ------------------------------------------------- products and their readers
+    const int grp = __shfl_sync(0xffffffffu, warp >> 2, 0), lrow = (warp & 3) * 32 + lane;
+    const bool issuer = __shfl_sync(0xffffffffu, (int)((warp & 3) == 0), 0);
+    const uint32_t t_s = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 128u * grp, d_s = tmem + 128u * grp;
+    auto waits = [&](int i, uint32_t par) {  // a failed wait is not repeated; barriers are still met
+      if (!failed && !mbar_wait(bar(i), par)) failed = 1;
+      __syncwarp();
+    };
+    auto group_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(2 + grp) : "memory"); };
+    // columns of a product: 128 tokens, or the rows in sixteens
+    const int n_cols = PASS == 0 ? kStepTok : (rows + 15) & ~15;
+    const uint32_t idc = idesc_f16(n_cols);
+    auto scores = [&](int j) {
+      const uint64_t q = smem_desc(sb + kOffQ), k = smem_desc(sb + kOffK + (j & 1) * 2 * kPart);
+      const uint64_t x = PASS == 0 ? q : k, y = PASS == 0 ? k : q;
+#pragma unroll 1
+      for (int part = 0; part < 3; ++part) {  // lo . hi, hi . lo, hi . hi
+        const uint64_t px = x + (part == 0 ? kPart >> 4 : 0), py = y + (part == 1 ? kPart >> 4 : 0);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) tc_mma(d_s, px + kstep(ks), py + kstep(ks), idc, (part | ks) != 0);
       }
+      tc_commit(bar(kSFull + grp));
+      tc_commit(bar(kKEmpty + (j & 1)));
+    };
+    if (grp == 0) {  // queries: raw operand, turned by the tensor cores, back as scaled hi + lo
+      const int64_t row = r0 + lrow;
+      const bool mine = lrow < rows;
+      const int64_t tok = mine ? row / a.gq : 0;
+      const int hq = h * a.gq + (mine ? (int)(row % a.gq) : 0);
+      put_query_row(sm + kOffQ, lrow,
+                    reinterpret_cast<const uint4*>(a.q + b * a.qs[0] + hq * a.qs[1] + tok * a.qs[2]), mine);
+      fence_async();
+      group_sync();
+      if (issuer) {
+        waits(kImg, 0);
+        tc_fence_after();
+        if (elect_one() && !failed) {
+          const uint64_t dx = smem_desc(sb + kOffQ), di = smem_desc(sb + kOffK);
+#pragma unroll 1
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              tc_mma(d_s, dx + kstep(ks), di + kstep(ks) + part * (kPart >> 4), idesc_f16(128), (part | ks) != 0);
+          tc_commit(bar(kQRot));
+        }
+        __syncwarp();
+      }
+      waits(kQRot, 0);
+      tc_fence_after();
+      uint8_t* qh = sm + kOffQ + lrow * 128;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t r[32];
+        tc_ld32(t_s + 32 * c, r);
+        tc_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int ch = 4 * c + k;
+          uint4 hi, lo;
+          split8(r + 8 * k, ms.qscale + 8 * ch, hi, lo);
+          uint8_t* o = qh + (ch >> 3) * 16384 + (((ch & 7) ^ (lrow & 7)) << 4);
+          *reinterpret_cast<uint4*>(o) = hi;
+          *reinterpret_cast<uint4*>(o + kPart) = lo;
+        }
+      }
+      tc_fence_before();
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kQFull));
+    }
+    if (issuer && grp < nb) {
+      waits(kQFull, 0);
+      waits(kKFull + grp, 0);
+      tc_fence_after();
+      if (elect_one() && !failed) scores(grp);
+      __syncwarp();
+    }
+    // pass 0: the row on this lane
+    int64_t end = 0;
+    if (PASS == 0 && lrow < rows) {
+      end = a.causal ? len - cl + (r0 + lrow) / a.gq + 1 : len;
+      if (end > s1) end = s1;
+    }
+    const bool warp_on = PASS == 1 || (warp & 3) * 32 < rows;
+    float ref = -INFINITY, sum = 0.f;
+    int it = 0;
+#pragma unroll 1
+    for (int j = grp; j < nb; j += 2, ++it) {
+      waits(kSFull + grp, it & 1);
+      tc_fence_after();
+      const int64_t at = s0 + (int64_t)j * kStepTok;
+      if (PASS == 0) {
+        if (warp_on) {
+          const int64_t left = end - at;
+          const int cnt = left < 0 ? 0 : (left < kStepTok ? (int)left : kStepTok);
+          const bool whole = __all_sync(0xffffffffu, cnt == kStepTok);
+          const float mx = whole ? row_max<false>(t_s, cnt) : row_max<true>(t_s, cnt);
+          if (mx > ref) {
+            sum *= ex2(ref - mx);
+            ref = mx;
+          }
+          const float base = ref == -INFINITY ? 0.f : ref;
+          float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t r[32];
+            tc_ld32(t_s + 32 * c, r);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float p = ex2(__uint_as_float(r[e]) - base);
+              part[e & 3] += whole || 32 * c + e < cnt ? p : 0.f;
+            }
+          }
+          sum += (part[0] + part[1]) + (part[2] + part[3]);
+        }
+      } else {
+        // the token on this lane, over the rows in their order (four running sums)
+        const int tok = j * kStepTok + lrow;  // of the stretch
+        const bool all = !a.causal || at + kStepTok - 1 <= len - cl + r0 / a.gq;
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int c = 0; c < n_cols; c += 16) {
+          uint32_t r[16];
+          tc_ld16(t_s + c, r);
+          tc_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const float4 st = *reinterpret_cast<const float4*>(&ms.stat[c + e]);
+            float p0 = ex2(__uint_as_float(r[e]) - st.x), p1 = ex2(__uint_as_float(r[e + 1]) - st.z);
+            if (!all) {
+              const int2 en = *reinterpret_cast<const int2*>(&ms.end[c + e]);
+              p0 = tok < en.x ? p0 : 0.f;
+              p1 = tok < en.y ? p1 : 0.f;
+            }
+            part[e & 2] = fmaf(p0, st.y, part[e & 2]);
+            part[(e & 2) + 1] = fmaf(p1, st.w, part[(e & 2) + 1]);
+          }
+        }
+        const int64_t t = at + lrow;
+        if (t < s1) {
+          const float w = (part[0] + part[1]) + (part[2] + part[3]);
+          out[t] = in ? in[t] + w : w;
+        }
+      }
+      tc_fence_before();
+      group_sync();
+      if (issuer && j + 2 < nb) {
+        waits(kKFull + (j & 1), ((j + 2) >> 1) & 1);
+        tc_fence_after();
+        if (elect_one() && !failed) scores(j + 2);
+        __syncwarp();
+      }
+    }
+    if (PASS == 0) {
+      if (grp == 1) ms.stat[lrow] = make_float2(ref, sum);
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (grp == 0 && lrow < rows) {
+        const float2 o = ms.stat[lrow];
+        const float top = fmaxf(ref, o.x), t = top == -INFINITY ? 0.f : top;
+        ml[lrow] = make_float2(top, sum * ex2(ref - t) + o.y * ex2(o.x - t));
+      }
+    }
+  } else {
+    // ------------------------------------------------------ codes to operands
+    const int dw = warp - kReadWarps;
+    const uint32_t tab = sb + kOffTab, norms = key_norm_offset(a.kb, a.vb);
+    const KeyLane k0 = key_lane(ms.m, dw, lane, 16384, norms, tab), k1 = key_lane(ms.m, 15 - dw, lane, 16384, norms, tab);
+    const int64_t t0 = s0 / kTile;
+    const uint8_t* const base = a.packed + (a.sm.table ? (int64_t)h * a.sm.tile_bytes
+                                                       : ((int64_t)head * a.sm.n_tiles + t0) * a.sm.tile_bytes);
+    const int32_t* const pages = a.sm.table ? a.sm.table + (int64_t)b * a.sm.max_blocks + t0 : nullptr;
+    auto tile_at = [&](int t) {
+      return base + (pages ? (int64_t)__ldg(pages + t) * a.sm.hkv : (int64_t)t) * a.sm.tile_bytes;
+    };
+    KeyRaw r0k, r1k;
+    auto fetch = [&](const uint8_t* p) {
+      load_keys<5>(r0k, p, k0);
+      load_keys<5>(r1k, p, k1);
+    };
+    fetch(tile_at(0));
+    const uint8_t* next = nt > 1 ? tile_at(1) : nullptr;
+    if (!mbar_wait(bar(kQRot), 0)) failed = 1;  // the keys' buffers lie under the rotation image
+    __syncwarp();
+#pragma unroll 1
+    for (int t = 0; t < 2 * nb && !failed; ++t) {
+      const int j = t >> 1;
+      if (!(t & 1) && j >= 2 && !mbar_wait(bar(kKEmpty + (j & 1)), ((j >> 1) & 1) ^ 1)) { failed = 1; break; }
+      __syncwarp();
+      if (t < nt) {
+        const KeyRaw c0 = r0k, c1 = r1k;
+        if (next) fetch(next);  // in flight during this tile
+        next = t + 2 < nt ? tile_at(t + 2) : nullptr;
+        if (t + kAheadW < nt && lane * 1024 + dw * 128 < (int)a.sm.tile_bytes)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(tile_at(t + kAheadW) + lane * 1024 + dw * 128));
+        const uint32_t row = sb + kOffK + (j & 1) * 2 * kPart + (t & 1) * 8192;
+        keys_by_code(k0, c0, tab, row, true, row + kPart + k0.col, 1024);
+        keys_by_code(k1, c1, tab, row, true, row + kPart + k1.col, 1024);
+      }
+      if (t & 1) {
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kKFull + (j & 1)));
+      }
+    }
   }
-  const int64_t tok = t * kTile + tid;
-  if (tid < kTile && tok < len) {
-    const int64_t o = b * a.ws[0] + h * a.ws[1] + tok;
-    a.w_out[o] = (a.w_in ? a.w_in[o] : 0.f) + w;
+  if (failed) atomicOr(a.status, kStatusTimeout);
+  if (__syncthreads_or(failed)) {  // nothing in flight may outlive the block (bounded waits)
+    if (warp == 0 || warp == 4) {
+      if (elect_one()) {
+        tc_commit(bar(kDrain + (warp >> 2)));
+        mbar_wait(bar(kDrain + (warp >> 2)), 0);
+      }
+    }
+    if (tid == 0) mbar_wait(bar(kImg), 0);
   }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(tmem));
 }
 
-ChunkArgs chunk_args(const gtq_plan* p, const uint8_t* packed, int64_t T, const SeqMap& sm,
-                     const gtq_chunk& c, const __half* q) {
-  ChunkArgs a = {};
+// Several row tiles: their sums, in order.
+__global__ void __launch_bounds__(256) add_kernel(const __grid_constant__ WeightArgs a) {
+  const int head = blockIdx.y, b = head / a.hkv, h = head % a.hkv;
+  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (t >= a.sm.len(b, a.T)) return;
+  const int64_t n_rows = chunk_len(a.chunk_lens, a.n, b) * a.gq;
+  const int tiles = (int)((n_rows + kRowsW - 1) / kRowsW);
+  const int64_t o = b * a.ws[0] + h * a.ws[1] + t;
+  float w = 0.f;
+  for (int r = 0; r < tiles; ++r) w += a.part_w[((int64_t)r * a.n_heads + head) * a.T + t];
+  a.w_out[o] = a.w_in ? a.w_in[o] + w : w;
+}
+
+struct CutW {
+  int row_tiles, splits;
+  int64_t span, rows_pad;
+};
+CutW cut_of(const gtq_plan* p, int64_t T, int64_t n) {
+  CutW c;
+  const int64_t rows = n * p->g_q;
+  c.row_tiles = (int)((rows + kRowsW - 1) / kRowsW);
+  c.rows_pad = (int64_t)c.row_tiles * kRowsW;
+  // enough blocks to fill the SMs evenly; a block's set-up costs about as much as 4 steps
+  const int64_t units = (int64_t)p->n_heads * c.row_tiles, steps = (T + kStepTok - 1) / kStepTok;
+  double best = 1e300;
+  int64_t best_per = steps;
+  for (int64_t s = 1; s <= 256 && s <= steps; ++s) {
+    const int64_t per = (steps + s - 1) / s, parts = (steps + per - 1) / per;
+    const double cost = (double)((units * parts + p->n_sms - 1) / p->n_sms) * (per + 4.0);
+    if (cost < best * 0.999) {
+      best = cost;
+      best_per = per;
+    }
+    if (units * s > 64 * (int64_t)p->n_sms) break;
+  }
+  c.span = best_per * kStepTok;
+  c.splits = (int)((steps + best_per - 1) / best_per);
+  return c;
+}
+
+size_t stat_bytes(const gtq_plan* p, const CutW& c) {
+  return ((size_t)p->n_heads * c.splits * c.rows_pad * sizeof(float2) + 255) & ~(size_t)255;
+}
+
+}  // namespace
+
+size_t weights_workspace(const gtq_plan* p, int64_t T, int64_t n) {
+  const CutW c = cut_of(p, T, n);
+  return stat_bytes(p, c) + (c.row_tiles > 1 ? (size_t)c.row_tiles * p->n_heads * T * sizeof(float) : 0);
+}
+
+cudaError_t launch_weights(const gtq_plan* p, const uint8_t* packed, int64_t T, const SeqMap& sm,
+                           const gtq_chunk& ch, const __half* q, const float* w_in, float* w_out,
+                           const int64_t* ws, uint8_t* workspace, cudaStream_t s) {
+  const CutW c = cut_of(p, T, ch.n_tokens);
+  WeightArgs a = {};
   a.packed = packed;
   a.sm = sm;
   a.T = T;
   a.q = q;
-  for (int i = 0; i < 3; ++i) {
-    a.qs[i] = c.q_strides[i];
-    a.os[i] = c.out_strides[i];
-  }
-  a.n = c.n_tokens;
-  a.chunk_lens = c.chunk_lens_dev;
-  a.causal = c.causal;
+  for (int i = 0; i < 3; ++i) a.qs[i] = ch.q_strides[i];
+  a.n = ch.n_tokens;
+  a.chunk_lens = ch.chunk_lens_dev;
+  a.causal = ch.causal;
   a.gq = p->g_q;
   a.hkv = p->cfg.n_kv_heads;
   a.kb = p->cfg.k_bits;
   a.vb = p->cfg.v_bits;
   a.meta = p->d_meta;
-  a.mrow = p->d_mrow;
-  a.rv = p->tab.rot_v;
-  a.singles = reinterpret_cast<const uint8_t*>(p->tab.dec_image) + kTabSS;
-  return a;
-}
-
-}  // namespace
-
-size_t weights_workspace(const gtq_plan* p, int64_t, int64_t n) {
-  return (size_t)p->n_heads * n * p->g_q * sizeof(float2);
-}
-
-cudaError_t launch_weights(const gtq_plan* p, const uint8_t* packed, int64_t T, const SeqMap& sm,
-                           const gtq_chunk& c, const __half* q, const float* w_in, float* w_out,
-                           const int64_t* ws, uint8_t* workspace, cudaStream_t s) {
-  ChunkArgs a = chunk_args(p, packed, T, sm, c, q);
+  a.bimg_k = p->d_bimg;
+  a.dec_image = p->tab.dec_image;
   a.w_in = w_in;
   a.w_out = w_out;
   a.ws[0] = ws[0];
   a.ws[1] = ws[1];
-  a.stats = reinterpret_cast<float2*>(workspace);
-  cudaError_t e = cudaFuncSetAttribute(chunk_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sizeof(Shared));
+  a.row_tiles = c.row_tiles;
+  a.splits = c.splits;
+  a.n_heads = p->n_heads;
+  a.span = c.span;
+  a.rows_pad = c.rows_pad;
+  a.part_ml = reinterpret_cast<float2*>(workspace);
+  a.part_w = reinterpret_cast<float*>(workspace + stat_bytes(p, c));
+  a.status = p->d_status;
+  cudaError_t e = cudaFuncSetAttribute(weights_kernel<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemW);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
+    e = cudaFuncSetAttribute(weights_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemW);
   if (e != cudaSuccess) return e;
-  const int64_t rows = c.n_tokens * p->g_q;
-  chunk_kernel<true><<<dim3((unsigned)((rows + kRows - 1) / kRows), (unsigned)p->n_heads), kThreadsC,
-                       sizeof(Shared), s>>>(a);
-  weights_kernel<<<dim3((unsigned)((T + kTile - 1) / kTile), (unsigned)p->n_heads), kThreadsC,
-                   sizeof(Shared), s>>>(a);
+  const dim3 grid((unsigned)(c.row_tiles * c.splits), (unsigned)p->n_heads);
+  weights_kernel<0><<<grid, kThreadsW, kSmemW, s>>>(a);
+  weights_kernel<1><<<grid, kThreadsW, kSmemW, s>>>(a);
+  if (c.row_tiles > 1)
+    add_kernel<<<dim3((unsigned)((T + 255) / 256), (unsigned)p->n_heads), 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 
