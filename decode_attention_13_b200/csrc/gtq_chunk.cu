@@ -626,6 +626,62 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Chun
       make_uint2(pack_h2(acc.x * inv, acc.y * inv), pack_h2(acc.z * inv, acc.w * inv));
 }
 
+// One new token a sequence is a decode step: launch_decode reads codes straight into registers
+// and has nothing to set up for rows that are not there.  These two kernels are the difference:
+// queries and tickets before it, fp16 rows after it.
+__global__ void __launch_bounds__(128) token_in_kernel(const __half* q, int64_t qs0, int64_t qs1, int hq,
+                                                       uint4* rows, int n_rows, unsigned* tickets, int n_tickets) {
+  const int i = blockIdx.x * 128 + threadIdx.x;  // 16 bytes of a row
+  if (i < n_rows * 16) {
+    const int row = i >> 4;
+    rows[i] = reinterpret_cast<const uint4*>(q + (row / hq) * qs0 + (row % hq) * qs1)[i & 15];
+  }
+  for (int t = i; t < n_tickets; t += gridDim.x * 128) tickets[t] = 0;
+}
+__global__ void __launch_bounds__(128) token_out_kernel(const float4* rows, int n_rows, __half* out, int64_t os0,
+                                                        int64_t os1, int hq, const int32_t* chunk_lens) {
+  const int i = blockIdx.x * 128 + threadIdx.x;
+  if (i >= n_rows * 16) return;
+  const int row = i >> 4, b = row / hq;
+  if (chunk_lens && chunk_lens[b] < 1) return;
+  const float4 x = rows[2 * i], y = rows[2 * i + 1];
+  reinterpret_cast<uint4*>(out + b * os0 + (row % hq) * os1)[i & 15] =
+      make_uint4(pack_h2(x.x, x.y), pack_h2(x.z, x.w), pack_h2(y.x, y.y), pack_h2(y.z, y.w));
+}
+
+// Workspace of a decode step: queries, results, and the split-merge state that the plan's own
+// decodes keep in the plan.
+struct TokenSpace {
+  size_t rows, out, tickets, partials, total;
+  int n_rows, n_tickets;
+  explicit TokenSpace(const gtq_plan* p) {
+    n_rows = p->cfg.batch * p->cfg.n_q_heads;
+    n_tickets = p->n_units * kTicketStride;
+    rows = 0;
+    out = rows + (size_t)n_rows * kD * sizeof(__half);
+    tickets = out + (size_t)n_rows * kD * sizeof(float);
+    partials = (tickets + (size_t)n_tickets * sizeof(unsigned) + 255) & ~(size_t)255;
+    total = partials + (size_t)p->n_units * PartialSlots(decode_split_cap(p->n_sms, p->n_units)).total * 8 *
+                           kPartialStride * sizeof(float);
+  }
+};
+cudaError_t launch_token(const gtq_plan* p, const uint8_t* packed, int64_t T, const SeqMap& sm, const gtq_chunk& ch,
+                         const __half* q, __half* out, uint8_t* ws, cudaStream_t s) {
+  const TokenSpace t(p);
+  gtq_plan own = *p;  // the caller's workspace in the place of the plan's
+  own.d_tickets = reinterpret_cast<unsigned*>(ws + t.tickets);
+  own.d_partials = reinterpret_cast<float*>(ws + t.partials);
+  const int blocks = (t.n_rows * 16 + 127) / 128;
+  token_in_kernel<<<blocks, 128, 0, s>>>(q, ch.q_strides[0], ch.q_strides[1], p->cfg.n_q_heads,
+                                         reinterpret_cast<uint4*>(ws + t.rows), t.n_rows, own.d_tickets, t.n_tickets);
+  cudaError_t e = launch_decode(&own, packed, T, ws + t.rows, GTQ_DTYPE_FP16, reinterpret_cast<float*>(ws + t.out),
+                                sm, Fp16Kv(), s);
+  if (e != cudaSuccess) return e;
+  token_out_kernel<<<blocks, 128, 0, s>>>(reinterpret_cast<const float4*>(ws + t.out), t.n_rows, out,
+                                          ch.out_strides[0], ch.out_strides[1], p->cfg.n_q_heads, ch.chunk_lens_dev);
+  return cudaGetLastError();
+}
+
 // How a call is cut: rows per block and splits of the tokens.
 struct Cut {
   int nq, row_tiles, splits;
@@ -669,6 +725,7 @@ Cut cut_of(const gtq_plan* p, int64_t T, int64_t n) {
 }  // namespace
 
 size_t chunk_workspace(const gtq_plan* p, int64_t T, int64_t n) {
+  if (n == 1) return TokenSpace(p).total;
   const Cut c = cut_of(p, T, n);
   if (c.splits <= 1) return 256;
   const size_t slots = (size_t)p->n_heads * c.splits * c.rows_pad;
@@ -678,6 +735,8 @@ size_t chunk_workspace(const gtq_plan* p, int64_t T, int64_t n) {
 cudaError_t launch_chunk(const gtq_plan* p, const uint8_t* packed, int64_t T, const SeqMap& sm,
                          const gtq_chunk& ch, const __half* q, __half* out, uint8_t* workspace,
                          cudaStream_t s) {
+  // (16 sequences x 4 KV heads of 7 queries, up to 16384 tokens each: 213 us as a chunk of one row)
+  if (ch.n_tokens == 1) return launch_token(p, packed, T, sm, ch, q, out, workspace, s);
   const Cut c = cut_of(p, T, ch.n_tokens);
   ChunkArgs a = {};
   a.packed = packed;

@@ -2,23 +2,24 @@
 // and last tokens and those with the largest weights stay, and their codes move
 // to another packed cache.  Two launches.
 //
-// select_kernel: one cluster of up to 8 blocks per head.  The weight that the
-// last chosen token has is found digit by digit (11, 11 and 10 bits of the
-// weight's order-preserving integer): each block counts the digits of its own
-// stretch of tokens, the cluster adds the counts through distributed shared
-// memory, and every block finds the digit where the count from the top passes
-// what is still wanted.  A last pass writes the indices in order: tokens above
-// that weight, and as many with exactly that weight, lowest index first, as are
-// missing.  It reads the weights four times (once from HBM, then from L2) and is
-// bound by the latency of its passes.
+// select_kernel: one cluster of up to 8 blocks per head.  Each block holds its stretch
+// of tokens in shared memory as order-preserving integers of their weights (HBM is
+// read once; tokens beyond that memory are read again from L2).  The weight that the
+// last chosen token has is found digit by digit (11, 11 and 10 bits): each block
+// counts the digits of its stretch, the cluster adds the counts through distributed
+// shared memory, and every block finds the digit where the count from the top passes
+// what is still wanted.  Then each thread counts 16 neighbouring tokens, one prefix sum
+// gives it its place, and it writes the indices of those that stay: tokens above that
+// weight, and as many with exactly that weight, lowest index first, as are missing.
+// Bound by the latencies of its dozen block- and cluster-wide steps.
 //
 // move_kernel: one block per new tile and head.  The tiles that its 64 tokens
-// come from arrive by bulk copy, kBatch at a time; a thread owns portions of the
-// new tile (all codes of 8 or 16 of its tokens in one slot or pair of dims), puts
-// them together in registers from two-word reads of the old tiles, and adds them
-// to the tile in shared memory, which leaves in full.  Bound by the bytes of the
-// source tiles (HBM reads them in sectors that hold the codes of many tokens) and
-// by the instructions of taking codes apart.
+// come from arrive by bulk copy, a batch at a time; a thread owns portions of the
+// new tile (all codes of 8 or 16 of its tokens in one slot or pair of dims), shifts
+// them together in registers from two-word reads of the old tiles, and adds them to
+// the tile in shared memory, which leaves in full.  The bytes of the source tiles are
+// its floor (HBM reads them in sectors that hold the codes of many tokens); taking codes
+// apart and together costs about as much.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -34,8 +35,10 @@ constexpr int kSelThreads = 1024;
 constexpr int kSelBins = 2048;
 constexpr int kSelCluster = 8;       // blocks per head at most (portable cluster size)
 constexpr int kSelTokens = 4096;     // tokens that are worth a block of their own
+constexpr int kPer = 16;             // neighbouring tokens of a thread
+constexpr int kHeld = 32768;         // tokens of a block that stay in shared memory
 constexpr int kMoveThreads = 256;
-constexpr int kBatch = 8;            // source tiles in shared memory at once
+constexpr int kMaxBatch = 12;        // source tiles in shared memory at once, at most
 
 struct EvictArgs {
   const float* w;
@@ -53,6 +56,8 @@ struct EvictArgs {
   uint8_t* dst_packed;
   const HeadMeta* meta;
   int kb, vb;
+  int held;   // select: tokens in shared memory
+  int batch;  // move: source tiles in shared memory
 };
 
 // Larger weight, larger integer; -0 as +0, NaN below everything.
@@ -89,7 +94,9 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
   return before + x - v;
 }
 
-__global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a) {
+__global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ EvictArgs a) {
+  extern __shared__ uint32_t keys[];  // token i of the stretch at i + i / 16: a thread's 16 neighbours
+                                      // then lie in as many banks as its warp's need
   __shared__ int hist[kSelBins];
   __shared__ int warp_sums[32];
   __shared__ int found[2];   // digit, and the count above it
@@ -102,28 +109,36 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a) {
   const int64_t n_keep = len < a.keep ? len : a.keep;
   const int64_t first = a.first < len ? a.first : len;
   const int64_t last = len - a.recent > first ? len - a.recent : first;  // [first, last) compete
-  int64_t want = n_keep - (first + len - last);
+  int want = (int)(n_keep - (first + len - last));
   const float* w = a.w + b * a.ws[0] + h * a.ws[1];
-  // this block's stretch, a multiple of the block's threads
+  // this block's stretch, a multiple of the threads' neighbours
   const int64_t part = (len + blocks - 1) / blocks;
-  const int64_t per = (part + kSelThreads - 1) / kSelThreads * kSelThreads;
-  const int64_t t0 = per * rank < len ? per * rank : len, t1 = t0 + per < len ? t0 + per : len;
+  const int64_t per = (part + kPer - 1) / kPer * kPer;
+  const int64_t t0 = per * rank < len ? per * rank : len;
+  const int n = (int)((t0 + per < len ? t0 + per : len) - t0);
+  const int c0 = (int)(first - t0 < 0 ? 0 : (first - t0 < n ? first - t0 : n));
+  const int c1 = (int)(last - t0 < 0 ? 0 : (last - t0 < n ? last - t0 : n));  // [c0, c1) compete
+  w += t0;
   const bool all = n_keep == len;  // nothing is left out (uniform over the cluster)
+  const int held = n < a.held ? n : a.held;
+  auto key_at = [&](int i) { return i < held ? keys[i + (i >> 4)] : order_key(w[i]); };
   uint32_t prefix = 0;
   if (!all) {
+    for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
+#pragma unroll 4
+    for (int i = tid; i < held; i += kSelThreads) keys[i + (i >> 4)] = order_key(w[i]);
+    __syncthreads();
     int shift = 32;
     for (int pass = 0; pass < 3; ++pass) {
       const int bits = pass < 2 ? 11 : 10;
       const uint32_t above = pass == 0 ? 0u : ~0u << shift;
       shift -= bits;
-      for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      for (int64_t base = t0; base < t1; base += kSelThreads) {
-        const int64_t t = base + tid;
-        bool on = t < t1 && t >= first && t < last;
+      for (int base = 0; base < n; base += kSelThreads) {
+        const int i = base + tid;
+        bool on = i >= c0 && i < c1;
         int bin = -1;
         if (on) {
-          const uint32_t k = order_key(w[t]);
+          const uint32_t k = key_at(i);
           on = (k & above) == prefix;
           bin = on ? (int)((k >> shift) & ((1u << bits) - 1)) : -1;
         }
@@ -140,85 +155,103 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a) {
       }
       cluster.sync();
       // bins from the top, two per thread: digit d = bins - 1 - i
-      const int n_bins = 1 << bits;
-      int c[2];
+      const int n_bins = 1 << bits, d0 = n_bins - 1 - 2 * tid;
+      int c[2] = {0, 0};
+      if (d0 > 0)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int d = n_bins - 1 - (2 * tid + e);
-        c[e] = 0;
-        if (d >= 0)
-          for (int r = 0; r < blocks; ++r) c[e] += *cluster.map_shared_rank(&hist[d], r);
-      }
+        for (int r = 0; r < kSelCluster; ++r)
+          if (r < blocks) {
+            const int* other = cluster.map_shared_rank(hist, r);
+            c[0] += other[d0];
+            c[1] += other[d0 - 1];
+          }
       int total;
       const int before = block_scan(c[0] + c[1], warp_sums, total);
-      const int wanted = (int)want;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int over = before + (e ? c[0] : 0);
-        if (over < wanted && over + c[e] >= wanted) {
-          found[0] = n_bins - 1 - (2 * tid + e);
+        if (over < want && over + c[e] >= want) {
+          found[0] = d0 - e;
           found[1] = over;
         }
       }
       // no block clears its counts while another still reads them
       cluster.sync();
-      if (wanted > 0) {
+      if (want > 0) {
         prefix |= (uint32_t)found[0] << shift;
         want -= found[1];
       } else {  // only the first and last tokens stay: nothing is above the largest integer
         prefix = ~0u;
       }
+      for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
       __syncthreads();
     }
-    if (want <= 0) want = 0;
   }
   // want: how many of the tokens whose integer is `prefix` stay
-  auto klass = [&](int64_t t) {  // 2 stays, 1 at the weight, 0 goes
-    if (t >= t1) return 0;
-    if (all || t < first || t >= last) return 2;
-    const uint32_t k = order_key(w[t]);
+  auto klass = [&](int i) {  // 2 stays, 1 at the weight, 0 goes
+    if (all || i < c0 || i >= c1) return 2;
+    const uint32_t k = key_at(i);
     return k > prefix ? 2 : (k == prefix && want > 0 ? 1 : 0);
   };
+  int sure = 0, equal = 0;
+  for (int base = tid * kPer; base < n; base += kSelThreads * kPer)
+#pragma unroll 4
+    for (int i = base; i < base + kPer; ++i) {
+      const int c = i < n ? klass(i) : 0;
+      sure += c == 2;
+      equal += c == 1;
+    }
   if (tid < 2) counts[tid] = 0;
   __syncthreads();
-  int sure = 0, equal = 0;
-  for (int64_t t = t0 + tid; t < t1; t += kSelThreads) {
-    const int c = klass(t);
-    sure += c == 2;
-    equal += c == 1;
-  }
+  {
+    int s = sure, q = equal;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    sure += __shfl_xor_sync(0xffffffffu, sure, o);
-    equal += __shfl_xor_sync(0xffffffffu, equal, o);
-  }
-  if (lane == 0) {
-    atomicAdd(&counts[0], sure);
-    atomicAdd(&counts[1], equal);
+    for (int o = 16; o; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      q += __shfl_xor_sync(0xffffffffu, q, o);
+    }
+    if (lane == 0) {
+      atomicAdd(&counts[0], s);
+      atomicAdd(&counts[1], q);
+    }
   }
   cluster.sync();
-  int64_t out = 0, eq = 0;  // tokens kept, and tokens at the weight, before this block's
+  int64_t out = 0, eq = 0;  // tokens sure to stay, and tokens at the weight, before this block's
   for (int r = 0; r < rank; ++r) {
-    out += *cluster.map_shared_rank(&counts[0], r);
-    eq += *cluster.map_shared_rank(&counts[1], r);
+    const int* other = cluster.map_shared_rank(counts, r);
+    out += other[0];
+    eq += other[1];
   }
   cluster.sync();  // nothing of another block is read past this point
-  out += eq < want ? eq : want;
   int32_t* kept = a.kept + (int64_t)head * a.kept_stride;
   float* wo = a.w_out ? a.w_out + b * a.wos[0] + h * a.wos[1] : nullptr;
-  for (int64_t base = t0; base < t1; base += kSelThreads) {
-    const int64_t t = base + tid;
-    const int c = klass(t);
-    int n_eq, n_out;
-    const int eq_here = block_scan(c == 1, warp_sums, n_eq);
-    const bool stays = c == 2 || (c == 1 && eq + eq_here < want);
-    const int at = block_scan(stays, warp_sums, n_out);
-    if (stays) {
-      kept[out + at] = (int32_t)t;
-      if (wo) wo[out + at] = w[t];
+  for (int start = 0; start < n; start += kSelThreads * kPer) {
+    const int base = start + tid * kPer;
+    if (n > kSelThreads * kPer) {  // more than one round: this round's counts
+      sure = equal = 0;
+      for (int i = base; i < base + kPer; ++i) {
+        const int c = i < n ? klass(i) : 0;
+        sure += c == 2;
+        equal += c == 1;
+      }
     }
-    eq += n_eq;
-    out += n_out;
+    int n_sure, n_equal;
+    const int sure_before = block_scan(sure, warp_sums, n_sure);
+    const int equal_before = block_scan(equal, warp_sums, n_equal);
+    // of the tokens at the weight, the first `want` of the head stay
+    int64_t e = eq + equal_before;
+    int64_t at = out + sure_before + (e < want ? e : want);
+    for (int i = base; i < base + kPer && i < n; ++i) {
+      const int c = klass(i);
+      if (c == 2 || (c == 1 && e < want)) {
+        kept[at] = (int32_t)(t0 + i);
+        if (wo) wo[at] = w[i];
+        ++at;
+      }
+      e += c == 1;
+    }
+    out += n_sure;
+    eq += n_equal;
   }
   for (int64_t i = n_keep + (int64_t)rank * kSelThreads + tid; i < a.fill; i += (int64_t)blocks * kSelThreads)
     kept[i] = -1;
@@ -235,12 +268,11 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t* x, int at) {
   return __funnelshift_r(x[i], x[i + 1], at & 31);
 }
 
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(EvictArgs a, int* status) {
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ EvictArgs a, int* status) {
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ HeadMeta m;
-  __shared__ int src_tile[kTile];    // distinct source tiles, in order
-  __shared__ uint8_t slot_of[kTile]; // token -> its place in that list
-  __shared__ uint8_t tok_in[kTile];  // token -> its index in its source tile
+  __shared__ int src_tile[kTile];     // distinct source tiles, in order
+  __shared__ uint16_t tok[kTile];     // token: place of its tile in that list << 8 | its index there
   __shared__ int n_src;
   __shared__ __align__(8) uint64_t bar;
   const int head = blockIdx.y, b = head / a.hkv;
@@ -253,9 +285,6 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(EvictArgs a, int* st
   const int tb = (int)a.src.tile_bytes;
   uint32_t* out = reinterpret_cast<uint32_t*>(sm);
   const uint32_t stage = (uint32_t)tb + 16;  // a word behind each tile may be read
-  for (int i = tid; i < tb / 16; i += kMoveThreads) reinterpret_cast<uint4*>(sm)[i] = make_uint4(0, 0, 0, 0);
-  for (int i = tid; i < (int)(sizeof(HeadMeta) / 4); i += kMoveThreads)
-    reinterpret_cast<uint32_t*>(&m)[i] = reinterpret_cast<const uint32_t*>(a.meta + head)[i];
   if (tid < 32) {  // which tiles the tokens come from: they are in order
     const int32_t* kept = a.kept + (int64_t)head * a.kept_stride + tile * kTile;
     int before = 0;
@@ -270,11 +299,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(EvictArgs a, int* st
       const bool fresh = s >= 0 && st != up;
       const unsigned f = __ballot_sync(0xffffffffu, fresh);
       const int at = before + __popc(f & ((2u << lane) - 1)) - 1;
-      if (s >= 0) {
-        slot_of[i] = (uint8_t)at;
-        tok_in[i] = (uint8_t)(s & 63);
-        if (fresh) src_tile[at] = st;
-      }
+      tok[i] = s >= 0 ? (uint16_t)(at << 8 | (s & 63)) : (uint16_t)0xffff;  // behind the last: in no batch
+      if (fresh) src_tile[at] = st;
       before += __popc(f);
       prev_last = __shfl_sync(0xffffffffu, st, 31);
     }
@@ -284,11 +310,14 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(EvictArgs a, int* st
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
   }
+  for (int i = tid; i < tb / 16; i += kMoveThreads) reinterpret_cast<uint4*>(sm)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = tid; i < (int)(sizeof(HeadMeta) / 4); i += kMoveThreads)
+    reinterpret_cast<uint32_t*>(&m)[i] = reinterpret_cast<const uint32_t*>(a.meta + head)[i];
   __syncthreads();
   const int kb = a.kb, vb = a.vb;
   bool ok = true;
-  for (int s0 = 0, round = 0; s0 < n_src && ok; s0 += kBatch, ++round) {
-    const int n = min(kBatch, n_src - s0);
+  for (int s0 = 0, round = 0; s0 < n_src && ok; s0 += a.batch, ++round) {
+    const int n = min(a.batch, n_src - s0);
     if (tid == 0) {
       asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(&bar)),
                    "r"((uint32_t)(n * tb)) : "memory");
@@ -317,71 +346,87 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(EvictArgs a, int* st
       }
     }
     if (__syncthreads_or(!ok)) { ok = false; break; }
-    auto source = [&](int j) -> const uint32_t* {  // token j's old tile, or null if not in this batch
-      const int i = (int)slot_of[j] - s0;
-      return j < n_tok && i >= 0 && i < n ? reinterpret_cast<const uint32_t*>(sm + tb + i * stage) : nullptr;
+    // token j: words of its old tile (null: not in this batch), and its index there
+    auto source = [&](int j, int& js) -> const uint32_t* {
+      const int v = tok[j], i = (v >> 8) - s0;
+      js = v & 63;
+      return (unsigned)i < (unsigned)n ? reinterpret_cast<const uint32_t*>(sm + tb + i * stage) : nullptr;
     };
-    // keys: portion g of slot s holds the pairs of tokens g + 8 u, 2 w bits each
-    for (int i = tid; i < m.n_slots * 8; i += kMoveThreads) {
-      const int s = i >> 3, g = i & 7, w = m.slot_width[s], w2 = 2 * w;
-      const int area = 8 * m.slot_koff[s];
-      uint32_t acc[4] = {0, 0, 0, 0};
-      for (int u = 0; u < 8; ++u) {
-        const uint32_t* x = source(g + 8 * u);
-        if (!x) continue;
-        const int js = tok_in[g + 8 * u];
-        const uint32_t pair = bits_at(x, area + (js & 7) * 16 * w + (js >> 3) * w2) & ((1u << w2) - 1);
-        const int at = u * w2, q = at >> 5, sh = at & 31;
+    // keys: portion g of slot s holds the pairs of tokens g + 8 u, 2 w bits each; a thread's two
+    // slots share the tokens.  The pairs are shifted in from the last to the first.
+    {
+      const int g = tid & 7;
+      int w[2], area[2];
+      uint32_t acc[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (k == q) acc[k] |= pair << sh;
-          if (k == q + 1 && sh) acc[k] |= pair >> (32 - sh);
+      for (int k = 0; k < 2; ++k) {
+        const int s = (tid >> 3) + 32 * k;
+        w[k] = m.slot_width[s];
+        area[k] = 8 * m.slot_koff[s];
+      }
+#pragma unroll 2
+      for (int u = 7; u >= 0; --u) {
+        int js;
+        const uint32_t* x = source(g + 8 * u, js);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int w2 = 2 * w[k];
+          uint32_t pair = 0;
+          if (x) pair = bits_at(x, area[k] + (js & 7) * 8 * w2 + (js >> 3) * w2) & ((1u << w2) - 1);
+          acc[k][3] = __funnelshift_l(acc[k][2], acc[k][3], w2);
+          acc[k][2] = __funnelshift_l(acc[k][1], acc[k][2], w2);
+          acc[k][1] = __funnelshift_l(acc[k][0], acc[k][1], w2);
+          acc[k][0] = (acc[k][0] << w2) | pair;
         }
       }
-      // 16 w bits at a multiple of 16 bits
-      uint16_t* o = reinterpret_cast<uint16_t*>(sm) + (area >> 4) + g * w;
-      for (int k = 0; k < w; ++k) o[k] |= (uint16_t)(acc[k >> 1] >> (16 * (k & 1)));
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {  // 16 w bits at a multiple of 16 bits
+        uint16_t* o = reinterpret_cast<uint16_t*>(sm) + (area[k] >> 4) + g * w[k];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < w[k]) o[i] |= (uint16_t)(acc[k][i >> 1] >> (16 * (i & 1)));
+      }
     }
-    // values: portion (i8, g, c) holds dims 16 i8 + g, + 8 of 16 tokens, 32 codes
+    // values: portion (i8, g, c) holds dims 16 i8 + g and + 8 of the tokens 16 a + 8 b + 2 c + l: for
+    // every (a, b) the codes of (dim, l) = (0, 0), (0, 1), (1, 0), (1, 1).  A token's two codes lie
+    // 2 vb bits apart in the old tile as they do in the new one.
     if (vb) {
-      const uint32_t mask = (1u << vb) - 1;
-      for (int p = tid; p < 256; p += kMoveThreads) {
-        const int c = p & 3, ig = p >> 2;
-        uint32_t acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int k = 0; k < 16; ++k) {
-          const int j = 16 * (k >> 2) + 8 * ((k >> 1) & 1) + 2 * c + (k & 1);
-          const uint32_t* x = source(j);
-          if (!x) continue;
-          const int js = tok_in[j];
-          const int xs = 8 * (js >> 4) + 4 * ((js >> 3) & 1) + (js & 1);
-          const uint32_t v = bits_at(x, 8192 * kb + (ig * 4 + ((js & 7) >> 1)) * 32 * vb + xs * vb);
-          const int xd = 8 * (k >> 2) + 4 * ((k >> 1) & 1) + (k & 1);
+      static_assert(kMoveThreads == 256, "one portion a thread");
+      const uint32_t code = (1u << vb) - 1, both = code | code << (2 * vb);
+      const int c = tid & 3, area = 8192 * kb + (tid >> 2) * 128 * vb;
+      uint32_t acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 2
+      for (int ab = 7; ab >= 0; --ab) {
+        uint32_t four = 0;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t code = (v >> (2 * e * vb)) & mask;
-            const int at = (xd + 2 * e) * vb, q = at >> 5, sh = at & 31;
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-              if (r == q) acc[r] |= code << sh;
-              if (r == q + 1 && sh) acc[r] |= code >> (32 - sh);
-            }
+        for (int l = 0; l < 2; ++l) {
+          int js;
+          const uint32_t* x = source(8 * ab + 2 * c + l, js);
+          if (x) {
+            const int xs = 4 * (js >> 3) + (js & 1);
+            four |= (bits_at(x, area + ((js & 7) >> 1) * 32 * vb + xs * vb) & both) << (l * vb);
           }
         }
-        uint32_t* o = out + 256 * kb + p * vb;
+        // shift the portion by 4 vb bits (a whole word at vb = 8)
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-          if (r < vb) o[r] |= acc[r];
+        for (int r = 7; r > 0; --r)
+          if (r < vb) acc[r] = __funnelshift_lc(acc[r - 1], acc[r], 4 * vb);
+        acc[0] = __funnelshift_lc(0u, acc[0], 4 * vb) | four;
       }
+      uint32_t* o = out + 256 * kb + tid * vb;
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < vb) o[r] |= acc[r];
     }
     // norms: row of 64 fp16, token j at (j & 7) * 8 + (j >> 3); the value norms, then the groups'
     const int n_rows = (vb ? 1 : 0) + m.n_groups;
     for (int i = tid; i < n_rows * kTile; i += kMoveThreads) {
-      const int row = i >> 6, j = i & 63;
-      const uint32_t* x = source(j);
+      const int row = i >> 6, at = i & 63, j = (at & 7) * 8 + (at >> 3);  // entry `at` is of token j
+      int js;
+      const uint32_t* x = source(j, js);
       if (!x) continue;
-      const int js = tok_in[j];
       const int o = 512 * (kb + vb) + row * 64;
-      reinterpret_cast<uint16_t*>(sm)[o + (j & 7) * 8 + (j >> 3)] =
+      reinterpret_cast<uint16_t*>(sm)[o + at] =
           reinterpret_cast<const uint16_t*>(x)[o + (js & 7) * 8 + (js >> 3)];
     }
     __syncthreads();  // the batch is read before the next one lands on it
@@ -424,7 +469,13 @@ cudaError_t launch_evict(const gtq_plan* p, const uint8_t* src, int64_t T, const
   a.vb = p->cfg.v_bits;
   int blocks = 1;
   while (blocks < kSelCluster && T > (int64_t)blocks * kSelTokens) blocks *= 2;
+  const int64_t stretch = (T + blocks - 1) / blocks + kPer;
+  a.held = (int)std::min<int64_t>(stretch, kHeld);
+  const size_t sel_smem = (size_t)(a.held + a.held / 16 + 1) * sizeof(uint32_t);
+  cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sel_smem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
+  cfg.dynamicSmemBytes = sel_smem;
   cfg.gridDim = dim3((unsigned)blocks, (unsigned)p->n_heads);
   cfg.blockDim = dim3(kSelThreads);
   cfg.stream = s;
@@ -435,10 +486,15 @@ cudaError_t launch_evict(const gtq_plan* p, const uint8_t* src, int64_t T, const
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, select_kernel, a);
+  e = cudaLaunchKernelEx(&cfg, select_kernel, a);
   if (e != cudaSuccess) return e;
   const int64_t most = std::min(ev.keep, T);
-  const size_t smem = p->tile_bytes + kBatch * (p->tile_bytes + 16);
+  // source tiles of a new tile: about T / keep and two cut ones; as many at once as leave room for
+  // two blocks on an SM
+  const int64_t span = (T + most - 1) / most + 2;
+  const int64_t room = 110 * 1024 / (int64_t)(p->tile_bytes + 16) - 1;
+  a.batch = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(span, kMaxBatch), room));
+  const size_t smem = p->tile_bytes + a.batch * (p->tile_bytes + 16);
   e = cudaFuncSetAttribute(move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   move_kernel<<<dim3((unsigned)((most + kTile - 1) / kTile), (unsigned)p->n_heads), kMoveThreads, smem, s>>>(
