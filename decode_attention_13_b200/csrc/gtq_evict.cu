@@ -94,10 +94,13 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
   return before + x - v;
 }
 
+// What lies behind the held keys in dynamic shared memory.
+__device__ __forceinline__ uint32_t* list_space(uint32_t* keys, int held) { return keys + held + held / 16 + 1; }
+
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ EvictArgs a) {
   extern __shared__ uint32_t keys[];  // token i of the stretch at i + i / 16: a thread's 16 neighbours
                                       // then lie in as many banks as its warp's need
-  __shared__ int hist[kSelBins];
+  __shared__ __align__(16) int hist[kSelBins];
   __shared__ int warp_sums[32];
   __shared__ int found[2];   // digit, and the count above it
   __shared__ int counts[2];  // this block's tokens that are sure to stay, and those at the weight
@@ -133,47 +136,55 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
       const int bits = pass < 2 ? 11 : 10;
       const uint32_t above = pass == 0 ? 0u : ~0u << shift;
       shift -= bits;
-      for (int base = 0; base < n; base += kSelThreads) {
-        const int i = base + tid;
-        bool on = i >= c0 && i < c1;
-        int bin = -1;
-        if (on) {
-          const uint32_t k = key_at(i);
-          on = (k & above) == prefix;
-          bin = on ? (int)((k >> shift) & ((1u << bits) - 1)) : -1;
-        }
-        // equal digits are common (weights of 0, near-equal exponents): the lanes that
-        // agree with the first one count once
-        const unsigned live = __ballot_sync(0xffffffffu, on);
-        if (live) {
-          const int lead = __ffs(live) - 1;
-          const int same = __shfl_sync(0xffffffffu, bin, lead);
-          const unsigned agree = __ballot_sync(0xffffffffu, on && bin == same);
-          if (lane == lead) atomicAdd(&hist[same], __popc(agree));
-          else if (on && bin != same) atomicAdd(&hist[bin], 1);
+      // equal digits are common: a weight of 0 is counted apart, and a thread's run of one
+      // digit is added at once
+      const int zero_bin = ((0x80000000u & above) == prefix) ? (int)((0x80000000u >> shift) & ((1u << bits) - 1)) : -1;
+      int zeros = 0, run = -1, run_n = 0;
+#pragma unroll 4
+      for (int i = c0 + tid; i < c1; i += kSelThreads) {
+        const uint32_t k = key_at(i);
+        const int bin = (int)((k >> shift) & ((1u << bits) - 1));
+        if (k == 0x80000000u) {
+          zeros += zero_bin >= 0;
+        } else if ((k & above) == prefix) {
+          if (bin != run) {
+            if (run_n) atomicAdd(&hist[run], run_n);
+            run = bin;
+            run_n = 0;
+          }
+          ++run_n;
         }
       }
+      if (run_n) atomicAdd(&hist[run], run_n);
+      zeros = __reduce_add_sync(0xffffffffu, zeros);
+      if (lane == 0 && zeros) atomicAdd(&hist[zero_bin], zeros);
       cluster.sync();
-      // bins from the top, two per thread: digit d = bins - 1 - i
-      const int n_bins = 1 << bits, d0 = n_bins - 1 - 2 * tid;
-      int c[2] = {0, 0};
-      if (d0 > 0)
+      // digits from the top, four a thread (16 bytes of every block's counts)
+      const int n_bins = 1 << bits, d0 = n_bins - 4 - 4 * tid;
+      int c[4] = {0, 0, 0, 0};
+      if (d0 >= 0) {
+        int4 v[kSelCluster];
+#pragma unroll
+        for (int r = 0; r < kSelCluster; ++r)
+          if (r < blocks) v[r] = *reinterpret_cast<const int4*>(cluster.map_shared_rank(hist, r) + d0);
 #pragma unroll
         for (int r = 0; r < kSelCluster; ++r)
           if (r < blocks) {
-            const int* other = cluster.map_shared_rank(hist, r);
-            c[0] += other[d0];
-            c[1] += other[d0 - 1];
+            c[0] += v[r].w;
+            c[1] += v[r].z;
+            c[2] += v[r].y;
+            c[3] += v[r].x;
           }
+      }
       int total;
-      const int before = block_scan(c[0] + c[1], warp_sums, total);
+      int over = block_scan(c[0] + c[1] + c[2] + c[3], warp_sums, total);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int over = before + (e ? c[0] : 0);
+      for (int e = 0; e < 4; ++e) {
         if (over < want && over + c[e] >= want) {
-          found[0] = d0 - e;
+          found[0] = d0 + 3 - e;
           found[1] = over;
         }
+        over += c[e];
       }
       // no block clears its counts while another still reads them
       cluster.sync();
@@ -193,14 +204,23 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     const uint32_t k = key_at(i);
     return k > prefix ? 2 : (k == prefix && want > 0 ? 1 : 0);
   };
-  int sure = 0, equal = 0;
-  for (int base = tid * kPer; base < n; base += kSelThreads * kPer)
-#pragma unroll 4
-    for (int i = base; i < base + kPer; ++i) {
-      const int c = i < n ? klass(i) : 0;
-      sure += c == 2;
-      equal += c == 1;
+  // a thread's 16 neighbours as bits: sure to stay, at the weight
+  auto classes = [&](int base, uint32_t& stay, uint32_t& at_weight) {
+    stay = at_weight = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int c = base + k < n ? klass(base + k) : 0;
+      stay |= (uint32_t)(c == 2) << k;
+      at_weight |= (uint32_t)(c == 1) << k;
     }
+  };
+  uint32_t stay = 0, at_weight = 0;
+  int sure = 0, equal = 0;
+  for (int base = tid * kPer; base < n; base += kSelThreads * kPer) {
+    classes(base, stay, at_weight);
+    sure += __popc(stay);
+    equal += __popc(at_weight);
+  }
   if (tid < 2) counts[tid] = 0;
   __syncthreads();
   {
@@ -216,41 +236,48 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     }
   }
   cluster.sync();
-  int64_t out = 0, eq = 0;  // tokens sure to stay, and tokens at the weight, before this block's
+  int64_t out = 0, eq = 0;  // tokens that stay, and tokens at the weight, before this block's
   for (int r = 0; r < rank; ++r) {
     const int* other = cluster.map_shared_rank(counts, r);
     out += other[0];
     eq += other[1];
   }
+  out += eq < want ? eq : want;
   cluster.sync();  // nothing of another block is read past this point
   int32_t* kept = a.kept + (int64_t)head * a.kept_stride;
   float* wo = a.w_out ? a.w_out + b * a.wos[0] + h * a.wos[1] : nullptr;
+  uint16_t* list = reinterpret_cast<uint16_t*>(list_space(keys, a.held));  // a round's kept tokens, in order
   for (int start = 0; start < n; start += kSelThreads * kPer) {
     const int base = start + tid * kPer;
-    if (n > kSelThreads * kPer) {  // more than one round: this round's counts
-      sure = equal = 0;
-      for (int i = base; i < base + kPer; ++i) {
-        const int c = i < n ? klass(i) : 0;
-        sure += c == 2;
-        equal += c == 1;
-      }
+    if (n > kSelThreads * kPer) {  // more than one round: this round's classes
+      classes(base, stay, at_weight);
+      sure = __popc(stay);
+      equal = __popc(at_weight);
     }
     int n_sure, n_equal;
     const int sure_before = block_scan(sure, warp_sums, n_sure);
     const int equal_before = block_scan(equal, warp_sums, n_equal);
     // of the tokens at the weight, the first `want` of the head stay
-    int64_t e = eq + equal_before;
-    int64_t at = out + sure_before + (e < want ? e : want);
-    for (int i = base; i < base + kPer && i < n; ++i) {
-      const int c = klass(i);
-      if (c == 2 || (c == 1 && e < want)) {
-        kept[at] = (int32_t)(t0 + i);
-        if (wo) wo[at] = w[i];
-        ++at;
-      }
-      e += c == 1;
+    const int64_t room = want - eq > 0 ? want - eq : 0;
+    int left = (int)(room > equal_before ? room - equal_before : 0);
+    int at = sure_before + (int)(equal_before < room ? equal_before : room);
+    uint32_t both = stay | at_weight;
+    while (both) {
+      const int k = __ffs(both) - 1;
+      both &= both - 1;
+      const bool tie = (at_weight >> k) & 1u;
+      if (!tie || left > 0) list[at++] = (uint16_t)(tid * kPer + k);
+      left -= tie;
     }
-    out += n_sure;
+    __syncthreads();
+    const int total = n_sure + (int)(n_equal < room ? n_equal : room);
+    for (int r = tid; r < total; r += kSelThreads) {
+      const int i = start + list[r];
+      kept[out + r] = (int32_t)(t0 + i);
+      if (wo) wo[out + r] = w[i];
+    }
+    __syncthreads();
+    out += total;
     eq += n_equal;
   }
   for (int64_t i = n_keep + (int64_t)rank * kSelThreads + tid; i < a.fill; i += (int64_t)blocks * kSelThreads)
@@ -471,7 +498,8 @@ cudaError_t launch_evict(const gtq_plan* p, const uint8_t* src, int64_t T, const
   while (blocks < kSelCluster && T > (int64_t)blocks * kSelTokens) blocks *= 2;
   const int64_t stretch = (T + blocks - 1) / blocks + kPer;
   a.held = (int)std::min<int64_t>(stretch, kHeld);
-  const size_t sel_smem = (size_t)(a.held + a.held / 16 + 1) * sizeof(uint32_t);
+  const size_t sel_smem = (size_t)(a.held + a.held / 16 + 1) * sizeof(uint32_t) +
+                          std::min<int64_t>(stretch, kSelThreads * kPer) * sizeof(uint16_t);
   cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sel_smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
