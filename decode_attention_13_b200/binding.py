@@ -56,6 +56,9 @@ ABI_FUNCTIONS = (
 )
 
 
+_I64x4 = ctypes.c_int64 * 4
+
+
 class GtqError(RuntimeError):
     def __init__(self, code: int, where: str):
         self.code = code
@@ -380,16 +383,17 @@ def gtq_decode_attn_full(plan: Plan, packed, T: int, q, out, layout=None, kv=Non
 
 
 def _rope_tensor(cfg, x, y, batch, tokens, name):
-    if y is None:
-        y = x
-    if x.dim() != 4 or tuple(x.shape) != tuple(y.shape):
-        raise ValueError("%s and its output must be 4-D [batch, heads, tokens, head_dim] of one shape" % name)
-    if x.shape[3] != cfg.head_dim or x.shape[0] != batch or x.shape[2] != tokens:
+    shape = x.shape
+    if len(shape) != 4 or shape[3] != cfg.head_dim or shape[0] != batch or shape[2] != tokens:
         raise ValueError("%s must be [%d, heads, %d, %d]" % (name, batch, tokens, cfg.head_dim))
-    if x.element_size() != (2 if cfg.dtype == DTYPE_FP16 else 4) or y.dtype != x.dtype:
-        raise ValueError("%s and its output must have the config's dtype" % name)
-    return gtq_rope_tensor(_ptr(x), _ptr(y), int(x.shape[1]), 0, _strides4(x, None),
-                           _strides4(y, None))
+    st = _I64x4(*x.stride())
+    if x.element_size() != (2 if cfg.dtype == DTYPE_FP16 else 4):
+        raise ValueError("%s must have the config's dtype" % name)
+    if y is None:
+        return gtq_rope_tensor(x.data_ptr(), x.data_ptr(), shape[1], 0, st, st)
+    if y.shape != shape or y.dtype != x.dtype:
+        raise ValueError("%s and its output must have one shape and dtype" % name)
+    return gtq_rope_tensor(x.data_ptr(), y.data_ptr(), shape[1], 0, st, _I64x4(*y.stride()))
 
 
 def gtq_rope(cfg: gtq_rope_config, q=None, q_out=None, k=None, k_out=None, positions=None, pos0=0,
@@ -400,21 +404,27 @@ def gtq_rope(cfg: gtq_rope_config, q=None, q_out=None, k=None, k_out=None, posit
     first = q if q is not None else k
     if first is None:
         raise ValueError("gtq_rope needs q or k")
-    batch, tokens = int(first.shape[0]), int(first.shape[2])
-    pos_stride = 0
+    if first.dim() != 4:
+        raise ValueError("gtq_rope takes [batch, heads, tokens, head_dim]")
+    batch, _, tokens, _ = first.shape
+    pos_stride = pos_ptr = 0
     if positions is not None:
-        if positions.element_size() != 8 or positions.shape[-1] != tokens or (
-                positions.dim() == 2 and positions.shape[0] != batch) or positions.dim() > 2:
+        ps = positions.shape
+        if positions.element_size() != 8 or not ps or ps[-1] != tokens or len(ps) > 2 or (
+                len(ps) == 2 and ps[0] != batch):
             raise ValueError("positions must be int64 [batch, tokens] or [tokens]")
-        if tokens > 1 and positions.stride(-1) != 1:
+        st = positions.stride()
+        if tokens > 1 and st[-1] != 1:
             raise ValueError("positions must be dense along tokens")
-        pos_stride = int(positions.stride(0)) if positions.dim() == 2 and batch > 1 else 0
-    tq = None if q is None else _rope_tensor(cfg, q, q_out, batch, tokens, "q")
-    tk = None if k is None else _rope_tensor(cfg, k, k_out, batch, tokens, "k")
-    rc = _lib.gtq_rope(ctypes.byref(cfg), batch, tokens, _ptr(positions), pos_stride, int(pos0),
-                       None if tq is None else ctypes.byref(tq),
-                       None if tk is None else ctypes.byref(tk), _stream(stream))
-    _check(rc, "gtq_rope")
+        if len(ps) == 2 and batch > 1:
+            pos_stride = st[0]
+        pos_ptr = positions.data_ptr()
+    tq = None if q is None else ctypes.byref(_rope_tensor(cfg, q, q_out, batch, tokens, "q"))
+    tk = None if k is None else ctypes.byref(_rope_tensor(cfg, k, k_out, batch, tokens, "k"))
+    rc = _lib.gtq_rope(ctypes.byref(cfg), batch, tokens, pos_ptr, pos_stride, pos0, tq, tk,
+                       _stream(stream))
+    if rc != GTQ_OK:
+        _check(rc, "gtq_rope")
 
 
 def _chunk(plan, q, out, chunk_lens, causal):

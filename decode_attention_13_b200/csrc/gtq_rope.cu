@@ -14,6 +14,9 @@
 //     writes, which makes y = x safe.
 //   * V is the widest vector (16 bytes at most) that divides rotary_dim / 2, the
 //     copied rest, every stride and both addresses.
+//   * Loads in flight come from many threads (2048 an SM): one item at a time measured
+//     faster than two or four a thread (32768 positions of 40 heads, fp16, 0.67 GB: 123,
+//     131 and 175 us).
 #include <algorithm>
 #include <cmath>
 
@@ -24,6 +27,17 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kMaxPairs = 128;
+
+// Division by a number known at launch: one multiplication where that is exact (dividends up to
+// `most` with most * d below 2^32), else a division.
+struct Divisor {
+  uint32_t d, m;
+  void set(uint32_t by, uint64_t most) {
+    d = by;
+    m = by > 1 && most * by < (1ull << 32) ? (uint32_t)((1ull << 32) / by + 1) : 0;
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return m ? __umulhi(n, m) : n / d; }
+};
 
 struct RopeSide {
   const uint8_t* x;
@@ -41,6 +55,8 @@ struct RopeArgs {
   int pairs;       // rotary_dim / 2
   int rot_items;   // pairs / V
   int items;       // rot_items + copied vectors
+  int per_tok;     // items of a position: all heads'
+  Divisor by_tok, by_items;
   float magnitude;
   int backward;
   double turns[kMaxPairs];  // f_i / (2 pi)
@@ -57,11 +73,13 @@ __device__ __forceinline__ void from_f(__half& o, float f) { o = __float2half_rn
 __device__ __forceinline__ void from_f(float& o, float f) { o = f; }
 
 template <typename E, int V, bool HALF, int TOK>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ float2 cs[TOK][kMaxPairs];
+  __shared__ int64_t seq[TOK];  // sequence of each position
   const int tid = threadIdx.x;
   const int64_t row0 = (int64_t)blockIdx.x * TOK;
   const int n_tok = (int)(a.n_rows - row0 < TOK ? a.n_rows - row0 : TOK);
+  if (tid < n_tok) seq[tid] = (row0 + tid) / a.tokens;
   for (int i = tid; i < n_tok * a.pairs; i += kRopeThreads) {
     const int r = i / a.pairs, j = i - r * a.pairs;
     const int64_t row = row0 + r, b = row / a.tokens, t = row - b * a.tokens;
@@ -72,19 +90,18 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     cs[r][j] = make_float2(c * a.magnitude, (a.backward ? -s : s) * a.magnitude);
   }
   __syncthreads();
-  const int heads = a.t[0].heads + a.t[1].heads;
-  const int per_tok = heads * a.items, total = n_tok * per_tok;
+  const int total = n_tok * a.per_tok;
+  using W = Vec<E, V>;
   for (int i = tid; i < total; i += kRopeThreads) {
-    const int r = i / per_tok, k = i - r * per_tok;
-    int h = k / a.items;
-    const int item = k - h * a.items;
+    const int r = TOK == 1 ? 0 : (int)a.by_tok.div((uint32_t)i), in_tok = i - r * a.per_tok;
+    int h = (int)a.by_items.div((uint32_t)in_tok);
+    const int item = in_tok - h * a.items;
     const bool second = h >= a.t[0].heads;
     const RopeSide& sd = a.t[second ? 1 : 0];
     if (second) h -= a.t[0].heads;
-    const int64_t row = row0 + r, b = row / a.tokens, t = row - b * a.tokens;
+    const int64_t b = seq[r], t = row0 + r - b * a.tokens;
     const E* x = reinterpret_cast<const E*>(sd.x + b * sd.xs[0] + h * sd.xs[1] + t * sd.xs[2]);
     E* y = reinterpret_cast<E*>(sd.y + b * sd.ys[0] + h * sd.ys[1] + t * sd.ys[2]);
-    using W = Vec<E, V>;
     if (item < a.rot_items) {
       const int o0 = HALF ? item * V : 2 * item * V;
       const int o1 = HALF ? o0 + a.pairs : o0 + V;
@@ -195,6 +212,9 @@ cudaError_t launch_rope(const gtq_rope_config& c, int64_t batch, int64_t tokens,
   while (v > 1 && align % (uint64_t)(v * es)) v /= 2;
   a.rot_items = a.pairs / v;
   a.items = a.rot_items + (c.head_dim - c.rotary_dim) / v;
+  a.per_tok = (a.t[0].heads + a.t[1].heads) * a.items;
+  a.by_tok.set((uint32_t)a.per_tok, 4ull * a.per_tok);
+  a.by_items.set((uint32_t)a.items, (uint64_t)a.per_tok);
   const bool half = c.rope_pairing == GTQ_PAIRING_HALF;
   if (es == 2) {
     switch (v) {
