@@ -82,12 +82,10 @@ __device__ __forceinline__ void split8(const uint32_t* r, const float* scale, ui
   uint32_t h[4], l[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    float x = __uint_as_float(r[2 * e]) * scale[2 * e], y = __uint_as_float(r[2 * e + 1]) * scale[2 * e + 1];
-    x = fminf(fmaxf(x, -65504.f), 65504.f);
-    y = fminf(fmaxf(y, -65504.f), 65504.f);
-    h[e] = pack_h2(x, y);
+    const float x = __uint_as_float(r[2 * e]) * scale[2 * e], y = __uint_as_float(r[2 * e + 1]) * scale[2 * e + 1];
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(h[e]) : "f"(y), "f"(x));
     const __half2 hh = *reinterpret_cast<__half2*>(&h[e]);
-    l[e] = pack_h2(x - __low2float(hh), y - __high2float(hh));
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(l[e]) : "f"(y - __high2float(hh)), "f"(x - __low2float(hh)));
   }
   hi = make_uint4(h[0], h[1], h[2], h[3]);
   lo = make_uint4(l[0], l[1], l[2], l[3]);

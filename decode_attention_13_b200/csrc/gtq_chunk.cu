@@ -14,7 +14,7 @@
 //     while no product on it runs).
 //     The first warp of each group of four also issues the group's products, as soon as the
 //     group has written its P: one hand-off less than a warp of its own.
-//   * warps 8-15       tiles of codes to operands (gtq_dequant.cuh): keys run two tiles ahead
+//   * warps 8-15       tiles of codes to operands (gtq_dequant.cuh): keys run a step ahead
 //     of values, and a warp's loads of the one are in flight while it works on the other.
 //     (24 warps, 16 of them here, measured 1.4 times slower: at 80 registers the loops spill.)
 // With 129 rows or more (NQ = 2) the two softmax groups take 128 rows each: while
@@ -43,7 +43,6 @@ constexpr int kSoftWarps = 8;
 constexpr int kDqWarps = 8;
 constexpr int kChunkThreads = 32 * (kSoftWarps + kDqWarps);
 constexpr int kBlockTok = 128;     // tokens of a step
-constexpr int kAhead = 6;          // packed tiles between a prefetch and its use
 constexpr int kSplitSlots = 8;     // slots (pairs of coordinates) with a low part
 constexpr float kRescale = 8.f;    // growth of the maximum (log2) that moves the reference
 
@@ -71,7 +70,7 @@ struct Map {
 };
 struct Misc {
   alignas(16) HeadMeta m;
-  alignas(16) float qscale[kD];
+  alignas(16) float qscale[2][kD];  // each softmax group's
   uint64_t bar[16];
   uint32_t tmem;
 };
@@ -159,11 +158,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
   const int head = blockIdx.y, b = head / a.hkv, h = head % a.hkv;
   const int rt = blockIdx.x % a.row_tiles, sp = blockIdx.x / a.row_tiles;
   const int64_t len = a.sm.len(b, a.T), cl = chunk_len(a.chunk_lens, a.n, b), n_rows = cl * a.gq;
-  const int64_t r0 = (int64_t)rt * (128 * NQ);
+  const int64_t r0 = (int64_t)rt * (128 * NQ);  // (rows fit 28 bits: 2^20 tokens of 128 heads)
   if (r0 >= n_rows) return;
   // tokens [s0, s1) of this block: its stretch, as far as its last row sees
   const int64_t last_row = (r0 + 128 * NQ < n_rows ? r0 + 128 * NQ : n_rows) - 1;
-  int64_t seen = a.causal ? len - cl + last_row / a.gq + 1 : len;
+  int64_t seen = a.causal ? len - cl + (int)last_row / a.gq + 1 : len;
   if (seen < 0) seen = 0;
   const int64_t s0 = sp * a.span;
   const int64_t s1 = seen < s0 + a.span ? seen : s0 + a.span;
@@ -204,9 +203,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     mbar_expect_tx(bar(kImg), kImage);
     bulk_load(sb + M::image, a.bimg_k + (size_t)head * kImage, kImage, bar(kImg));
   }
-  for (int i = tid; i < (int)(sizeof(HeadMeta) / 4); i += kChunkThreads)
-    reinterpret_cast<uint32_t*>(&ms.m)[i] = reinterpret_cast<const uint32_t*>(a.meta + head)[i];
-  load_dequant_tables(sm + M::tab, a.dec_image, tid, kChunkThreads);
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(&ms.tmem)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -215,8 +211,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ms.tmem, 0);  // the same in all lanes, and known to be
-  if (tid < kD) ms.qscale[tid] = query_scale(ms.m, tid);
-  __syncthreads();
+  launch_dependents();
   int failed = 0;
 
   if (warp < kSoftWarps) {
@@ -224,10 +219,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     const int grp = __shfl_sync(0xffffffffu, warp >> 2, 0), lrow = (warp & 3) * 32 + lane;  // row within its 128
     const bool issuer = __shfl_sync(0xffffffffu, (int)((warp & 3) == 0), 0);
     const int tile = NQ == 2 ? grp : 0;
-    const int64_t row = r0 + 128 * tile + lrow;
+    const int row = (int)r0 + 128 * tile + lrow;
     const bool mine = row < n_rows;
-    const int64_t tok = mine ? row / a.gq : 0;
-    const int hq = h * a.gq + (mine ? (int)(row % a.gq) : 0);
+    const int tok = mine ? row / a.gq : 0;
+    const int hq = h * a.gq + (mine ? row - tok * a.gq : 0);
     const bool warp_on = __any_sync(0xffffffffu, mine);
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lane_off + 128u * grp, t_o = tmem + lane_off + 256u + 128u * grp;
@@ -270,6 +265,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     const int first = NQ == 2 ? 0 : grp, stride = NQ == 2 ? 1 : 2;  // the group's steps
     // raw queries -> operand, rotated by the tensor cores, back as scaled hi + lo
     if (NQ == 2 || grp == 0) {
+      ms.qscale[grp][lrow] = query_scale(a.meta[head], lrow);
       put_query_row(sm + M::qhi + tile * kQHi, lrow,
                     reinterpret_cast<const uint4*>(a.q + b * a.qs[0] + hq * a.qs[1] + tok * a.qs[2]), mine);
       fence_async();
@@ -295,7 +291,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         for (int k = 0; k < 4; ++k) {  // 8 coordinates each
           const int ch = 4 * c + k;
           uint4 hi, lo;
-          split8(r + 8 * k, ms.qscale + 8 * ch, hi, lo);
+          split8(r + 8 * k, ms.qscale[grp] + 8 * ch, hi, lo);
           *reinterpret_cast<uint4*>(qhi + (ch >> 3) * 16384 + (((ch & 7) ^ sw) << 4)) = hi;
           if (ch < 2) *reinterpret_cast<uint4*>(qlo + ch * 128) = lo;
         }
@@ -475,8 +471,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     }
   } else {
     // ------------------------------------------------------ codes to operands
-    const int dw = warp - kSoftWarps;
+    const int dw = warp - kSoftWarps, dtid = tid - 32 * kSoftWarps;
     const uint32_t tab = sb + M::tab;
+    for (int i = dtid; i < (int)(sizeof(HeadMeta) / 4); i += 32 * kDqWarps)
+      reinterpret_cast<uint32_t*>(&ms.m)[i] = reinterpret_cast<const uint32_t*>(a.meta + head)[i];
+    load_dequant_tables(sm + M::tab, a.dec_image, dtid, 32 * kDqWarps);
+    asm volatile("bar.sync 4, %0;" ::"n"(32 * kDqWarps) : "memory");
     // quads dw and 15 - dw of the keys, dims 16 dw .. of the values, of every tile
     const uint32_t norms = key_norm_offset(a.kb, a.vb);
     const KeyLane k0 = key_lane(ms.m, dw, lane, 16384, norms, tab);
@@ -484,95 +484,114 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     const bool low = dw < kSplitSlots / 4;  // slots of quad dw leave low parts
     const bool code0 = low || __any_sync(0xffffffffu, k0.w > 4), code1 = __any_sync(0xffffffffu, k1.w > 4);
     const uint32_t lo_lane = (uint32_t)dw * 128 + 16u * (lane & 7) + 4u * (lane >> 3);
-    // tile addresses: page numbers are read a tile ahead of their use
+    // addresses of a step's tiles: page numbers are read a step ahead of their use
     const int64_t t0 = s0 / kTile;
     const uint8_t* const base = a.packed + (a.sm.table ? (int64_t)h * a.sm.tile_bytes
                                                        : ((int64_t)head * a.sm.n_tiles + t0) * a.sm.tile_bytes);
     const int32_t* const pages = a.sm.table ? a.sm.table + (int64_t)b * a.sm.max_blocks + t0 : nullptr;
-    int page = pages ? __ldg(pages) : 0;
-    auto tile_at = [&](int t) {  // called once for every t < nt in order
-      const uint8_t* p = base + (pages ? (int64_t)page * a.sm.hkv : (int64_t)t) * a.sm.tile_bytes;
-      if (pages && t + 1 < nt) page = __ldg(pages + t + 1);
-      return p;
+    int page[2] = {0, 0};
+    auto read_pages = [&](int j) {
+      if (pages)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (2 * j + i < nt) page[i] = __ldg(pages + 2 * j + i);
     };
-    KeyRaw r0, r1;
-    ValueRaw rv;
-    auto fetch_keys = [&](const uint8_t* p) {
-      if (code0) load_keys<5>(r0, p, k0);
-      else load_keys<2>(r0, p, k0);
-      if (!code1) load_keys<2>(r1, p, k1);
+    auto tile_of = [&](int j, int i) {
+      return base + (pages ? (int64_t)page[i] * a.sm.hkv : (int64_t)(2 * j + i)) * a.sm.tile_bytes;
     };
-    auto put_keys = [&](int t, const uint8_t* p) {
-      const uint32_t dst = sb + M::k + ((t >> 1) & 1) * kKBuf, row = dst + (t & 1) * 8192;
-      if (code0) keys_by_code(k0, r0, tab, row, low, dst + 32768 + (t & 1) * 2048 + lo_lane, 256);
-      else keys_by_pair(k0, r0, row);
-      if (!code1) {
-        keys_by_pair(k1, r1, row);
-      } else {  // widths above 4 beyond the first half of the slots: fetched when they are due
-        KeyRaw r;
-        load_keys<5>(r, p, k1);
-        keys_by_code(k1, r, tab, row, false, 0, 0);
+    const uint8_t *kp[2], *vp[2];  // tiles of the keys in flight, and of the values due
+    KeyRaw r0[2], r1[2];
+    ValueRaw rv[2];
+    auto fetch_keys = [&](int j) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        kp[i] = tile_of(j, i);
+        if (2 * j + i >= nt) break;
+        if (code0) load_keys<5>(r0[i], kp[i], k0);
+        else load_keys<2>(r0[i], kp[i], k0);
+        if (!code1) load_keys<2>(r1[i], kp[i], k1);
+      }
+      read_pages(j + 1);
+    };
+    auto put_keys = [&](int j) {
+      const uint32_t dst = sb + M::k + (j & 1) * kKBuf;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (2 * j + i >= nt) break;  // rows behind the last tile: whatever they hold, their scores do not count
+        const uint32_t row = dst + i * 8192;
+        if (code0) keys_by_code(k0, r0[i], tab, row, low, dst + 32768 + i * 2048 + lo_lane, 256);
+        else keys_by_pair(k0, r0[i], row);
+        if (!code1) {
+          keys_by_pair(k1, r1[i], row);
+        } else {  // widths above 4 beyond the first half of the slots: fetched when they are due
+          KeyRaw r;
+          load_keys<5>(r, kp[i], k1);
+          keys_by_code(k1, r, tab, row, false, 0, 0);
+        }
       }
     };
-    const uint8_t *pa = tile_at(0), *pb = nullptr, *pc = nullptr;  // tiles v, v + 1, v + 2
-    fetch_keys(pa);
+    read_pages(0);
+    fetch_keys(0);
     // the keys' buffers lie under the rotation image
     if (!mbar_wait(bar(kQRot), 0)) failed = 1;
     __syncwarp();
-    // step by step: keys of tile t = v + 2, then values of tile v
+    if (!failed) {
+      put_keys(0);
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kKFull));
+      vp[0] = kp[0];
+      vp[1] = kp[1];
+      if (nb > 1) fetch_keys(1);
+    }
+    // step by step: the keys of step j + 1, then the values of step j (a fence costs as much as
+    // a portion's work: one for both)
 #pragma unroll 1
-    for (int t = 0; t < 2 * nb + 2 && !failed; ++t) {
-      const int v = t - 2;
-      const uint8_t* now = t == 0 ? pa : (t == 1 ? pb : pc);
-      if (v >= 0 && v < nt) load_values(rv, pa, a.kb, a.vb, dw, lane);
-      if (t < 2 * nb) {
-        const int j = t >> 1;
-        if (!(t & 1) && j >= 2 && !mbar_wait(bar(kKEmpty + (j & 1)), ((j >> 1) & 1) ^ 1)) { failed = 1; break; }
+    for (int j = 0; j < nb && !failed; ++j) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (2 * j + i < nt) load_values(rv[i], vp[i], a.kb, a.vb, dw, lane);
+      if (j + 1 < nb) {
+        if (j >= 1 && !mbar_wait(bar(kKEmpty + ((j + 1) & 1)), (((j + 1) >> 1) & 1) ^ 1)) { failed = 1; break; }
         __syncwarp();
-        // rows behind the last tile: whatever they hold, their scores do not count
-        if (t < nt) put_keys(t, now);
-        if (t & 1) {
-          fence_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kKFull + (j & 1)));
+        put_keys(j + 1);
+      }
+      const uint8_t *n0 = kp[0], *n1 = kp[1];
+      if (j + 2 < nb) fetch_keys(j + 2);  // in flight during the values
+      // and what is due two steps later, towards the L2 cache (an eighth of the tile's lines a warp)
+      if (lane * 1024 + dw * 128 < (int)a.sm.tile_bytes)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int t = 2 * (j + 4) + i;
+          if (t < nt)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                base + (pages ? (int64_t)__ldg(pages + t) * a.sm.hkv : (int64_t)t) * a.sm.tile_bytes + lane * 1024 +
+                dw * 128));
         }
-      }
-      // the next tile's keys, in flight during the values
-      const uint8_t* next = t + 1 < nt ? tile_at(t + 1) : nullptr;
-      if (next) fetch_keys(next);
-      // and what is due three steps on, towards the L2 cache (an eighth of the tile's lines a warp)
-      if (t + kAhead < nt && lane * 1024 < (int)a.sm.tile_bytes) {
-        const uint8_t* p = base + (pages ? (int64_t)__ldg(pages + t + kAhead) * a.sm.hkv : (int64_t)(t + kAhead)) * a.sm.tile_bytes;
-        if (lane * 1024 + dw * 128 < (int)a.sm.tile_bytes)
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(p + lane * 1024 + dw * 128));
-      }
-      if (v >= 0) {
-        const int j = v >> 1;
-        if (!(v & 1) && j >= 2 && !mbar_wait(bar(kVEmpty + (j & 1)), ((j >> 1) & 1) ^ 1)) { failed = 1; break; }
-        __syncwarp();
-        const uint32_t atom = M::v + (v & 3) * kVAtom;
+      if (j >= 2 && !mbar_wait(bar(kVEmpty + (j & 1)), ((j >> 1) & 1) ^ 1)) { failed = 1; break; }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int v = 2 * j + i;
+        const uint32_t atom = M::v + (2 * (j & 1) + i) * kVAtom;
         if (v < nt) {
           const int64_t left = s1 - (s0 + (int64_t)v * kTile);
           uint32_t n[8];
-          value_norms(rv, lane, left < kTile ? (int)left : kTile, n);
-          dequant_values(pa, a.kb, a.vb, dw, lane, rv, n, tab, sb + atom);
+          value_norms(rv[i], lane, left < kTile ? (int)left : kTile, n);
+          dequant_values(vp[i], a.kb, a.vb, dw, lane, rv[i], n, tab, sb + atom);
         } else {  // no tile: zeros, since the probabilities' zeros must not meet a NaN
-          for (int i = lane; i < 128; i += 32)
-            *reinterpret_cast<uint4*>(sm + atom + dw * 2048 + 16 * i) = make_uint4(0, 0, 0, 0);
+          for (int k = lane; k < 128; k += 32)
+            *reinterpret_cast<uint4*>(sm + atom + dw * 2048 + 16 * k) = make_uint4(0, 0, 0, 0);
         }
-        if (v & 1) {
-          fence_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kVFull + (j & 1)));
-        }
-        pa = pb;
-        pb = pc;
-        pc = next;
-      } else if (t == 0) {
-        pb = next;
-      } else {
-        pc = next;
       }
+      fence_async();
+      __syncwarp();
+      if (lane == 0) {
+        if (j + 1 < nb) mbar_arrive(bar(kKFull + ((j + 1) & 1)));
+        mbar_arrive(bar(kVFull + (j & 1)));
+      }
+      vp[0] = n0;
+      vp[1] = n1;
     }
   }
   if (failed) atomicOr(a.status, kStatusTimeout);
@@ -595,33 +614,59 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
   if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// One warp per row: the splits' outputs, weighted by what their maxima and sums say.
+// The splits' outputs of a row, weighted by what their maxima and sums say.  WPR warps a row: one
+// where there are many rows, eight where there are few rows of many splits.
+template <int WPR>
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ ChunkArgs a) {
-  const int head = blockIdx.y, b = head / a.hkv, h = head % a.hkv, lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  __shared__ float4 part[8][32];
+  __shared__ float part_sum[8];
+  const int head = blockIdx.y, b = head / a.hkv, h = head % a.hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = (int)blockIdx.x * (8 / WPR) + warp / WPR, mine = warp % WPR;
   const int64_t cl = chunk_len(a.chunk_lens, a.n, b);
-  if (row >= cl * a.gq) return;
+  wait_dependency();  // every block: this kernel ends after the one before it
+  if ((int64_t)(blockIdx.x * (8 / WPR)) >= cl * a.gq) return;
+  const bool on = row < cl * a.gq;
   const int64_t base = (int64_t)head * a.splits * a.rows_pad + row;
   float top = -INFINITY;
-  for (int s = lane; s < a.splits; s += 32) top = fmaxf(top, a.part_ml[base + s * a.rows_pad].x);
+  if (on)
+    for (int s = lane; s < a.splits; s += 32) top = fmaxf(top, a.part_ml[base + s * a.rows_pad].x);
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float total = 0.f;
   if (top != -INFINITY)
-    for (int s = 0; s < a.splits; ++s) {
+#pragma unroll 4
+    for (int s = mine; s < a.splits; s += WPR) {
       const float2 ml = a.part_ml[base + s * a.rows_pad];
       const float w = ml.y * ex2(ml.x - top);
-      if (!(w > 0.f)) continue;
-      const float4 o = reinterpret_cast<const float4*>(a.part_o + (base + s * a.rows_pad) * kD)[lane];
+      // (what a split without a visible token left is not read as a number)
+      const float4 o = w > 0.f ? reinterpret_cast<const float4*>(a.part_o + (base + s * a.rows_pad) * kD)[lane]
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
       acc.x = fmaf(w, o.x, acc.x);
       acc.y = fmaf(w, o.y, acc.y);
       acc.z = fmaf(w, o.z, acc.z);
       acc.w = fmaf(w, o.w, acc.w);
       total += w;
     }
+  if (WPR > 1) {
+    part[warp][lane] = acc;
+    if (lane == 0) part_sum[warp] = total;
+    __syncthreads();
+    if (mine) return;
+#pragma unroll
+    for (int k = 1; k < WPR; ++k) {
+      const float4 o = part[warp + k][lane];
+      acc.x += o.x;
+      acc.y += o.y;
+      acc.z += o.z;
+      acc.w += o.w;
+      total += part_sum[warp + k];
+    }
+  }
+  if (!on) return;
   const float inv = total > 0.f ? 1.f / total : 0.f;
-  __half* out = a.out + b * a.os[0] + (h * a.gq + row % a.gq) * a.os[1] + row / a.gq * a.os[2];
+  const int tok = row / a.gq;
+  __half* out = a.out + b * a.os[0] + (h * a.gq + row - tok * a.gq) * a.os[1] + tok * a.os[2];
   *reinterpret_cast<uint2*>(out + 4 * lane) =
       make_uint2(pack_h2(acc.x * inv, acc.y * inv), pack_h2(acc.z * inv, acc.w * inv));
 }
@@ -773,8 +818,10 @@ cudaError_t launch_chunk(const gtq_plan* p, const uint8_t* packed, int64_t T, co
   kernel<<<dim3((unsigned)(c.row_tiles * c.splits), (unsigned)p->n_heads), kChunkThreads, c.smem, s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || c.splits == 1) return e;
-  merge_kernel<<<dim3((unsigned)((ch.n_tokens * p->g_q + 7) / 8), (unsigned)p->n_heads), 256, 0, s>>>(a);
-  return cudaGetLastError();
+  const int64_t rows = ch.n_tokens * p->g_q;
+  if (c.splits >= 8)
+    return launch_overlapped(merge_kernel<8>, dim3((unsigned)rows, (unsigned)p->n_heads), 256, 0, s, a);
+  return launch_overlapped(merge_kernel<1>, dim3((unsigned)((rows + 7) / 8), (unsigned)p->n_heads), 256, 0, s, a);
 }
 
 }  // namespace gtq

@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
   const int64_t r0 = (int64_t)rt * kRowsW, s0 = sp * a.span;
   const int rows = (int)(n_rows - r0 < 0 ? 0 : (n_rows - r0 < kRowsW ? n_rows - r0 : kRowsW));
   int64_t seen = len;
-  if (PASS == 0 && a.causal && rows) seen = len - cl + (r0 + rows - 1) / a.gq + 1;
+  if (PASS == 0 && a.causal && rows) seen = len - cl + ((int)r0 + rows - 1) / a.gq + 1;
   const int64_t s1 = seen < s0 + a.span ? seen : s0 + a.span;
   float2* ml = a.part_ml + ((int64_t)head * a.splits + sp) * a.rows_pad + r0;
   float* out = nullptr;
@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
     }
   }
   if (rows == 0 || s0 >= s1) {
+    if (PASS == 1) wait_dependency();  // this kernel ends after the one before it
     if (PASS == 0) {
       for (int r = tid; r < rows; r += kThreadsW) ml[r] = make_float2(-INFINITY, 0.f);
     } else if (a.row_tiles == 1) {  // no row: what was there stays
@@ -138,35 +139,15 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
     mbar_expect_tx(bar(kImg), kImageBytes);
     bulk_load(sb + kOffK, a.bimg_k + (size_t)head * kImageBytes, kImageBytes, bar(kImg));
   }
-  for (int i = tid; i < (int)(sizeof(HeadMeta) / 4); i += kThreadsW)
-    reinterpret_cast<uint32_t*>(&ms.m)[i] = reinterpret_cast<const uint32_t*>(a.meta + head)[i];
-  load_dequant_tables(sm + kOffTab, a.dec_image, tid, kThreadsW);
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(su32(&ms.tmem)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-  }
-  if (PASS == 1 && tid >= kThreadsW - kRowsW) {  // every row's softmax, from its stretches
-    const int r = tid - (kThreadsW - kRowsW);
-    float top = -INFINITY, total = 0.f;
-    if (r < rows) {
-      const float2* p = a.part_ml + (int64_t)head * a.splits * a.rows_pad + r0 + r;
-      for (int s = 0; s < a.splits; ++s) top = fmaxf(top, p[s * a.rows_pad].x);
-      if (top != -INFINITY)
-        for (int s = 0; s < a.splits; ++s) {
-          const float2 v = p[s * a.rows_pad];
-          total += v.y * ex2(v.x - top);
-        }
-    }
-    ms.stat[r] = total > 0.f ? make_float2(top, 1.f / total) : make_float2(0.f, 0.f);
-    const int64_t end = (a.causal ? len - cl + (r0 + r) / a.gq + 1 : len) - s0;
-    ms.end[r] = r >= rows || end < 0 ? 0 : (end < a.span ? (int)end : (int)a.span);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ms.tmem, 0);
-  if (tid < kD) ms.qscale[tid] = query_scale(ms.m, tid);
-  __syncthreads();
+  launch_dependents();
   int failed = 0;
 
   if (warp < kReadWarps) {
@@ -195,10 +176,11 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
       tc_commit(bar(kKEmpty + (j & 1)));
     };
     if (grp == 0) {  // queries: raw operand, turned by the tensor cores, back as scaled hi + lo
-      const int64_t row = r0 + lrow;
+      const int row = (int)r0 + lrow;
       const bool mine = lrow < rows;
-      const int64_t tok = mine ? row / a.gq : 0;
-      const int hq = h * a.gq + (mine ? (int)(row % a.gq) : 0);
+      const int tok = mine ? row / a.gq : 0;
+      const int hq = h * a.gq + (mine ? row - tok * a.gq : 0);
+      ms.qscale[lrow] = query_scale(a.meta[head], lrow);
       put_query_row(sm + kOffQ, lrow,
                     reinterpret_cast<const uint4*>(a.q + b * a.qs[0] + hq * a.qs[1] + tok * a.qs[2]), mine);
       fence_async();
@@ -240,6 +222,28 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kQFull));
     }
+    if (PASS == 1) {  // every row's softmax, from its stretches; the other group turns the queries
+      if (grp == 1) {
+        wait_dependency();
+        const int r = lrow;
+        float top = -INFINITY, total = 0.f;
+        if (r < rows) {
+          const float2* p = a.part_ml + (int64_t)head * a.splits * a.rows_pad + r0 + r;
+#pragma unroll 4
+          for (int s = 0; s < a.splits; ++s) top = fmaxf(top, p[s * a.rows_pad].x);
+          if (top != -INFINITY)
+#pragma unroll 4
+            for (int s = 0; s < a.splits; ++s) {
+              const float2 v = p[s * a.rows_pad];
+              total += v.y * ex2(v.x - top);
+            }
+        }
+        ms.stat[r] = total > 0.f ? make_float2(top, 1.f / total) : make_float2(0.f, 0.f);
+        const int64_t end = (a.causal ? len - cl + ((int)r0 + r) / a.gq + 1 : len) - s0;
+        ms.end[r] = r >= rows || end < 0 ? 0 : (end < a.span ? (int)end : (int)a.span);
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+    }
     if (issuer && grp < nb) {
       waits(kQFull, 0);
       waits(kKFull + grp, 0);
@@ -250,9 +254,10 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
     // pass 0: the row on this lane
     int64_t end = 0;
     if (PASS == 0 && lrow < rows) {
-      end = a.causal ? len - cl + (r0 + lrow) / a.gq + 1 : len;
+      end = a.causal ? len - cl + ((int)r0 + lrow) / a.gq + 1 : len;
       if (end > s1) end = s1;
     }
+    const int64_t first_end = len - cl + (int)r0 / a.gq;  // last token that the first row sees
     const bool warp_on = PASS == 1 || (warp & 3) * 32 < rows;
     float ref = -INFINITY, sum = 0.f;
     int it = 0;
@@ -289,7 +294,7 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
       } else {
         // the token on this lane, over the rows in their order (four running sums)
         const int tok = j * kStepTok + lrow;  // of the stretch
-        const bool all = !a.causal || at + kStepTok - 1 <= len - cl + r0 / a.gq;
+        const bool all = !a.causal || at + kStepTok - 1 <= first_end;
         float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
         for (int c = 0; c < n_cols; c += 16) {
@@ -335,7 +340,11 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
     }
   } else {
     // ------------------------------------------------------ codes to operands
-    const int dw = warp - kReadWarps;
+    const int dw = warp - kReadWarps, dtid = tid - 32 * kReadWarps;
+    for (int i = dtid; i < (int)(sizeof(HeadMeta) / 4); i += 32 * kDqWarps)
+      reinterpret_cast<uint32_t*>(&ms.m)[i] = reinterpret_cast<const uint32_t*>(a.meta + head)[i];
+    load_dequant_tables(sm + kOffTab, a.dec_image, dtid, 32 * kDqWarps);
+    asm volatile("bar.sync 4, %0;" ::"n"(32 * kDqWarps) : "memory");
     const uint32_t tab = sb + kOffTab, norms = key_norm_offset(a.kb, a.vb);
     const KeyLane k0 = key_lane(ms.m, dw, lane, 16384, norms, tab), k1 = key_lane(ms.m, 15 - dw, lane, 16384, norms, tab);
     const int64_t t0 = s0 / kTile;
@@ -480,7 +489,8 @@ cudaError_t launch_weights(const gtq_plan* p, const uint8_t* packed, int64_t T, 
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)(c.row_tiles * c.splits), (unsigned)p->n_heads);
   weights_kernel<0><<<grid, kThreadsW, kSmemW, s>>>(a);
-  weights_kernel<1><<<grid, kThreadsW, kSmemW, s>>>(a);
+  e = launch_overlapped(weights_kernel<1>, grid, kThreadsW, kSmemW, s, a);
+  if (e != cudaSuccess) return e;
   if (c.row_tiles > 1)
     add_kernel<<<dim3((unsigned)((T + 255) / 256), (unsigned)p->n_heads), 256, 0, s>>>(a);
   return cudaGetLastError();
