@@ -234,6 +234,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       __syncwarp();
     };
     auto group_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(2 + grp) : "memory"); };
+    // NQ = 2: the groups take turns with the exponentials.  Both at once would share the unit for
+    // them, finish together and then share the tensor cores; in turns, one's products run during the
+    // other's exponentials.
+    auto my_turn = [&] { asm volatile("bar.sync %0, 256;" ::"r"(5 + grp) : "memory"); };
+    auto your_turn = [&] { asm volatile("bar.arrive %0, 256;" ::"r"(6 - grp) : "memory"); };
+    if (NQ == 2 && grp == 1) your_turn();
     // products of the group, issued by one lane of its first warp
     const uint32_t idc = idesc_f16(128);
     const uint32_t d_s = tmem + 128u * grp, d_o = tmem + 256u + 128u * grp;
@@ -317,10 +323,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     for (int j = first; j < nb; j += stride, ++it) {
       waits(kSFull + grp, it & 1);
       tc_fence_after();
+      const int64_t left = end - (s0 + (int64_t)j * kBlockTok);
+      const int cnt = left < 0 ? 0 : (left < kBlockTok ? (int)left : kBlockTok);
+      const bool whole = __all_sync(0xffffffffu, cnt == kBlockTok);
       if (warp_on) {
-        const int64_t left = end - (s0 + (int64_t)j * kBlockTok);
-        const int cnt = left < 0 ? 0 : (left < kBlockTok ? (int)left : kBlockTok);
-        const bool whole = __all_sync(0xffffffffu, cnt == kBlockTok);
         const float mx = whole ? row_max<false>(t_s, cnt) : row_max<true>(t_s, cnt);
         const bool grow = mx > ref + kRescale;  // also out of -inf
         if (__any_sync(0xffffffffu, grow)) {
@@ -341,9 +347,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
             tc_wait_st();
           }
         }
+      }
+      if (NQ == 2) my_turn();
+      if (warp_on) {
         const float base = ref == -INFINITY ? 0.f : ref;
         sum += whole ? row_exp<false>(t_s, cnt, base) : row_exp<true>(t_s, cnt, base);
       }
+      if (NQ == 2 && (grp == 0 || j + 1 < nb)) your_turn();
       tc_fence_before();
       group_sync();
       if (issuer) {
