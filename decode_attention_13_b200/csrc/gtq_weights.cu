@@ -14,6 +14,9 @@
 // The result is fp32, so scores are q (hi + lo) . k (hi + lo) without lo . lo: three
 // products of fp16 halves carry about 22 bits of each factor.
 //
+// With up to kKeepRows rows of a KV head, pass 0 leaves the scores themselves (4 bytes a row
+// and token) and kept_kernel takes the place of pass 1: reading them again costs less than
+// turning the codes into operands again (8 rows over 2 x 131072 tokens: 41 us for pass 1).
 // Rows beyond 128 of a KV head are more blocks, whose sums lie side by side in the
 // workspace until add_kernel joins them in order.
 #include <algorithm>
@@ -31,6 +34,7 @@ constexpr int kDqWarps = 8;
 constexpr int kThreadsW = 32 * (kReadWarps + kDqWarps);
 constexpr int kStepTok = 128;
 constexpr int kRowsW = 128;
+constexpr int kKeepRows = 64;  // rows whose scores are kept (8 bytes moved a row and token against about 1000 for pass 1)
 constexpr int kAheadW = 6;  // packed tiles between a prefetch and its use
 
 // shared memory: queries and two steps of keys, each fp16 hi and lo (two swizzled atoms a part)
@@ -74,10 +78,12 @@ struct WeightArgs {
   const float* w_in;
   float* w_out;
   int64_t ws[2];
-  int row_tiles, splits, n_heads;
+  int row_tiles, splits, n_heads, rows_kept;
   int64_t span, rows_pad;
   float2* part_ml;  // [heads][splits][rows_pad]
   float* part_w;    // [row tiles][heads][T], when there are several row tiles
+  float* kept;      // [heads][rows][kept_stride] scores, or null
+  int64_t kept_stride;
   int* status;
 };
 
@@ -278,11 +284,17 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
           }
           const float base = ref == -INFINITY ? 0.f : ref;
           float part[4] = {0.f, 0.f, 0.f, 0.f};
+          uint4* kept = a.kept ? reinterpret_cast<uint4*>(a.kept + ((int64_t)head * a.rows_kept + lrow) * a.kept_stride + at)
+                               : nullptr;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t r[32];
             tc_ld32(t_s + 32 * c, r);
             tc_wait_ld();
+            if (kept && lrow < rows)
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                kept[8 * c + e] = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               const float p = ex2(__uint_as_float(r[e]) - base);
@@ -400,6 +412,44 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
   if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(tmem));
 }
 
+// Kept scores: a thread takes one token and adds its weights over the rows, in order.
+__global__ void __launch_bounds__(256) kept_kernel(const __grid_constant__ WeightArgs a) {
+  __shared__ float2 stat[kKeepRows];
+  __shared__ int64_t end[kKeepRows];
+  const int head = blockIdx.y, b = head / a.hkv, h = head % a.hkv;
+  const int64_t len = a.sm.len(b, a.T), cl = chunk_len(a.chunk_lens, a.n, b);
+  const int rows = (int)(cl * a.gq), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  wait_dependency();
+  if ((int64_t)blockIdx.x * 256 >= len) return;
+  for (int r = warp; r < rows; r += 8) {  // every row's softmax, from its stretches
+    const float2* p = a.part_ml + (int64_t)head * a.splits * a.rows_pad + r;
+    float top = -INFINITY, total = 0.f;
+    for (int s = lane; s < a.splits; s += 32) top = fmaxf(top, p[s * a.rows_pad].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (top != -INFINITY)
+      for (int s = lane; s < a.splits; s += 32) total += p[s * a.rows_pad].y * ex2(p[s * a.rows_pad].x - top);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (lane == 0) {
+      stat[r] = total > 0.f ? make_float2(top, 1.f / total) : make_float2(0.f, 0.f);
+      end[r] = a.causal ? len - cl + r / a.gq + 1 : len;
+    }
+  }
+  __syncthreads();
+  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (t >= len) return;
+  const float* s = a.kept + (int64_t)head * a.rows_kept * a.kept_stride + t;
+  float part[4] = {0.f, 0.f, 0.f, 0.f};
+  // (a stretch that no row sees is not written: nothing is read where a row sees nothing)
+#pragma unroll 4
+  for (int r = 0; r < rows; ++r)
+    if (t < end[r]) part[r & 3] = fmaf(ex2(s[r * a.kept_stride] - stat[r].x), stat[r].y, part[r & 3]);
+  const float w = (part[0] + part[1]) + (part[2] + part[3]);
+  const int64_t o = b * a.ws[0] + h * a.ws[1] + t;
+  a.w_out[o] = a.w_in ? a.w_in[o] + w : w;
+}
+
 // Several row tiles: their sums, in order.
 __global__ void __launch_bounds__(256) add_kernel(const __grid_constant__ WeightArgs a) {
   const int head = blockIdx.y, b = head / a.hkv, h = head % a.hkv;
@@ -444,10 +494,14 @@ size_t stat_bytes(const gtq_plan* p, const CutW& c) {
   return ((size_t)p->n_heads * c.splits * c.rows_pad * sizeof(float2) + 255) & ~(size_t)255;
 }
 
+// tokens of a row of kept scores: whole steps are written
+int64_t kept_stride(const CutW& c) { return c.span * c.splits; }
+
 }  // namespace
 
 size_t weights_workspace(const gtq_plan* p, int64_t T, int64_t n) {
   const CutW c = cut_of(p, T, n);
+  if (n * p->g_q <= kKeepRows) return stat_bytes(p, c) + (size_t)p->n_heads * n * p->g_q * kept_stride(c) * sizeof(float);
   return stat_bytes(p, c) + (c.row_tiles > 1 ? (size_t)c.row_tiles * p->n_heads * T * sizeof(float) : 0);
 }
 
@@ -488,6 +542,13 @@ cudaError_t launch_weights(const gtq_plan* p, const uint8_t* packed, int64_t T, 
     e = cudaFuncSetAttribute(weights_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemW);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)(c.row_tiles * c.splits), (unsigned)p->n_heads);
+  if (ch.n_tokens * p->g_q <= kKeepRows) {
+    a.kept = a.part_w;
+    a.kept_stride = kept_stride(c);
+    a.rows_kept = (int)(ch.n_tokens * p->g_q);
+    weights_kernel<0><<<grid, kThreadsW, kSmemW, s>>>(a);
+    return launch_overlapped(kept_kernel, dim3((unsigned)((T + 255) / 256), (unsigned)p->n_heads), 256, 0, s, a);
+  }
   weights_kernel<0><<<grid, kThreadsW, kSmemW, s>>>(a);
   e = launch_overlapped(weights_kernel<1>, grid, kThreadsW, kSmemW, s, a);
   if (e != cudaSuccess) return e;
