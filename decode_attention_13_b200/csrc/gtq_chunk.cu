@@ -568,15 +568,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       }
       const uint8_t *n0 = kp[0], *n1 = kp[1];
       if (j + 2 < nb) fetch_keys(j + 2);  // in flight during the values
-      // and what is due two steps later, towards the L2 cache (an eighth of the tile's lines a warp)
-      if (lane * 1024 + dw * 128 < (int)a.sm.tile_bytes)
+      // and what is due two steps later, towards the L2 cache (the warps take turns)
+      if (lane == 0 && (j & 7) == dw)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int t = 2 * (j + 4) + i;
           if (t < nt)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(
-                base + (pages ? (int64_t)__ldg(pages + t) * a.sm.hkv : (int64_t)t) * a.sm.tile_bytes + lane * 1024 +
-                dw * 128));
+            bulk_prefetch(base + (pages ? (int64_t)__ldg(pages + t) * a.sm.hkv : (int64_t)t) * a.sm.tile_bytes,
+                          (uint32_t)a.sm.tile_bytes);
         }
       if (j >= 2 && !mbar_wait(bar(kVEmpty + (j & 1)), ((j >> 1) & 1) ^ 1)) { failed = 1; break; }
       __syncwarp();

@@ -384,8 +384,11 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
         const KeyRaw c0 = r0k, c1 = r1k;
         if (next) fetch(next);  // in flight during this tile
         next = t + 2 < nt ? tile_at(t + 2) : nullptr;
-        if (t + kAheadW < nt && lane * 1024 + dw * 128 < (int)a.sm.tile_bytes)
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(tile_at(t + kAheadW) + lane * 1024 + dw * 128));
+        if (t + kAheadW < nt && lane == 0 && (t & 7) == dw) {  // towards the L2 cache (the warps take turns)
+          const uint8_t* p = tile_at(t + kAheadW);
+          bulk_prefetch(p, 1024u * a.kb);
+          bulk_prefetch(p + norms, 1024u);
+        }
         const uint32_t row = sb + kOffK + (j & 1) * 2 * kPart + (t & 1) * 8192;
         keys_by_code(k0, c0, tab, row, true, row + kPart + k0.col, 1024);
         keys_by_code(k1, c1, tab, row, true, row + kPart + k1.col, 1024);
