@@ -49,29 +49,31 @@ constexpr float kRescale = 8.f;    // growth of the maximum (log2) that moves th
 // shared memory, from a 1024-byte boundary
 constexpr uint32_t kQHi = 32768;                    // queries of 128 rows, fp16 (two swizzled atoms)
 constexpr uint32_t kQLo = 4096;                     // their low parts, 16 coordinates
-constexpr uint32_t kKBuf = 32768 + 4096;            // keys of a step, and their low parts
-constexpr uint32_t kVAtom = 16384;                  // values of a packed tile
-constexpr uint32_t kImage = 65536;                  // a rotation, hi and lo
-template <int NQ>
+template <int NQ, bool PAIR>
 struct Map {
+  // the second operand's rows: all 128, or a CTA's half of them
+  static constexpr uint32_t atom = PAIR ? 8192 : 16384;     // 64 columns of them, swizzled
+  static constexpr uint32_t klo = 2 * atom;                 // keys of a step: two atoms, then their low parts
+  static constexpr uint32_t kbuf = klo + (PAIR ? 2048 : 4096);
+  static constexpr uint32_t image_bytes = 4 * atom;         // a rotation: hi and lo, two atoms each
   static constexpr uint32_t qhi = 0;
   static constexpr uint32_t qlo = qhi + NQ * kQHi;
   static constexpr uint32_t k = qlo + NQ * kQLo;
-  static constexpr uint32_t v = k + 2 * kKBuf;
-  static constexpr uint32_t tab = v + 4 * kVAtom;
-  static constexpr uint32_t misc = tab + kDqBytes;
+  static constexpr uint32_t v = k + 2 * kbuf;               // values of two steps, an atom a packed tile
   // before the steps: the keys' rotation image; after them: the values' image, then the low
   // parts of the outputs (their high parts lie where the queries were) and, for NQ = 1, the
   // second group's maxima and sums
   static constexpr uint32_t image = qlo;
-  static constexpr uint32_t olo = image + kImage;
+  static constexpr uint32_t olo = image + image_bytes;
+  static constexpr uint32_t olo_end = olo + NQ * 32768 + (NQ == 1 ? 1024 : 0), v_end = v + 4 * atom;
+  static constexpr uint32_t tab = olo_end > v_end ? olo_end : v_end;
+  static constexpr uint32_t misc = tab + kDqBytes;
   static constexpr uint32_t stat = tab - 1024;
-  static_assert(olo + NQ * 32768 <= (NQ == 1 ? stat : tab), "operands of the last product");
 };
 struct Misc {
   alignas(16) HeadMeta m;
   alignas(16) float qscale[2][kD];  // each softmax group's
-  uint64_t bar[16];
+  uint64_t bar[18];
   uint32_t tmem;
 };
 
@@ -86,6 +88,8 @@ constexpr int kQRot = 11;           // products of a rotation done
 constexpr int kQFull = 12;          // rotated queries written
 constexpr int kOFull = 13;          // all steps' products done
 constexpr int kDrain = 14;          // [2] after a failed wait: a group's products so far are done
+constexpr int kHand = 16;           // [2] pairs: a group is done in both CTAs (raw queries, turned queries, every
+                                    // step's probabilities, outputs)
 
 struct ChunkArgs {
   const uint8_t* packed;
@@ -144,9 +148,10 @@ __device__ __forceinline__ float row_exp(uint32_t s, int cnt, float ref) {
   return x + y;
 }
 
-template <int NQ>
+template <int NQ, bool PAIR>
 __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_constant__ ChunkArgs a) {
-  using M = Map<NQ>;
+  static_assert(NQ == 2 || !PAIR, "pairs have 512 rows");
+  using M = Map<NQ, PAIR>;
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sb = su32(sm);
   if (sb & 1023u) {  // the swizzled operands need it; there is no room to spare for a shift
@@ -156,12 +161,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
   Misc& ms = *reinterpret_cast<Misc*>(sm + M::misc);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int head = blockIdx.y, b = head / a.hkv, h = head % a.hkv;
-  const int rt = blockIdx.x % a.row_tiles, sp = blockIdx.x / a.row_tiles;
+  const int rank = PAIR ? cluster_rank() : 0;
+  const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+  const int rt = unit % a.row_tiles, sp = unit / a.row_tiles;
   const int64_t len = a.sm.len(b, a.T), cl = chunk_len(a.chunk_lens, a.n, b), n_rows = cl * a.gq;
-  const int64_t r0 = (int64_t)rt * (128 * NQ);  // (rows fit 28 bits: 2^20 tokens of 128 heads)
-  if (r0 >= n_rows) return;
-  // tokens [s0, s1) of this block: its stretch, as far as its last row sees
-  const int64_t last_row = (r0 + 128 * NQ < n_rows ? r0 + 128 * NQ : n_rows) - 1;
+  constexpr int kUnitRows = 128 * NQ * (PAIR ? 2 : 1);
+  const int64_t u0 = (int64_t)rt * kUnitRows;  // (rows fit 28 bits: 2^20 tokens of 128 heads)
+  if (u0 >= n_rows) return;
+  const int64_t r0 = u0 + rank * (128 * NQ);   // this CTA's own
+  // tokens [s0, s1) of this block: its stretch, as far as its (pair's) last row sees
+  const int64_t last_row = (u0 + kUnitRows < n_rows ? u0 + kUnitRows : n_rows) - 1;
   int64_t seen = a.causal ? len - cl + (int)last_row / a.gq + 1 : len;
   if (seen < 0) seen = 0;
   const int64_t s0 = sp * a.span;
@@ -184,13 +193,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
   const int nt = (int)((s1 - s0 + kTile - 1) / kTile);          // packed tiles
   const uint32_t bar0 = su32(ms.bar);
   auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+  auto wait_on = [&](int i, uint32_t par) { return PAIR ? mbar_wait_pair(bar(i), par) : mbar_wait(bar(i), par); };
+  auto commit = [&](int i) { PAIR ? tc_commit_pair(bar(i)) : tc_commit(bar(i)); };
+  // a CTA's share of an image's rows: all, or 64 of each atom
+  auto load_image = [&](const uint8_t* src) {
+    mbar_expect_tx(bar(kImg), M::image_bytes);
+    if (PAIR) {
+      for (int i = 0; i < 4; ++i)
+        bulk_load(sb + M::image + i * M::atom, src + i * 16384 + rank * M::atom, M::atom, bar(kImg));
+    } else {
+      bulk_load(sb + M::image, src, M::image_bytes, bar(kImg));
+    }
+  };
 
   // ---------------------------------------------------------------- set-up
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(kKFull + i), kDqWarps);
+      mbar_init(bar(kKFull + i), kDqWarps * (PAIR ? 2 : 1));
+      mbar_init(bar(kHand + i), 2);
       mbar_init(bar(kKEmpty + i), NQ);
-      mbar_init(bar(kVFull + i), kDqWarps);
+      mbar_init(bar(kVFull + i), kDqWarps * (PAIR ? 2 : 1));
       mbar_init(bar(kVEmpty + i), NQ);
       mbar_init(bar(kSFull + i), 1);
       mbar_init(bar(kDrain + i), 1);
@@ -200,15 +222,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     mbar_init(bar(kQFull), 4 * NQ);
     mbar_init(bar(kOFull), 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    mbar_expect_tx(bar(kImg), kImage);
-    bulk_load(sb + M::image, a.bimg_k + (size_t)head * kImage, kImage, bar(kImg));
+    load_image(a.bimg_k + (size_t)head * 65536);
   }
   if (warp == 0) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(&ms.tmem)));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    if (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(&ms.tmem)));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(&ms.tmem)));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync_all();  // the other CTA's barriers are there
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ms.tmem, 0);  // the same in all lanes, and known to be
   launch_dependents();
@@ -230,10 +257,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     const uint32_t sw = (uint32_t)(lrow & 7);
     // A wait that has failed is not repeated, but every barrier of the group is still met.
     auto waits = [&](int i, uint32_t par) {
-      if (!failed && !mbar_wait(bar(i), par)) failed = 1;
+      if (!failed && !wait_on(i, par)) failed = 1;
       __syncwarp();
     };
+    // The group has written an operand (or, with `img`, also an image is due): its issuer goes on.
+    // Pairs: when the same group of both CTAs has, the even CTA's issuer does.
+    int handed = 0;
     auto group_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(2 + grp) : "memory"); };
+    auto hand = [&](int img) -> bool {
+      group_sync();
+      if (!issuer) return false;
+      if (img >= 0) waits(kImg, (uint32_t)img);
+      if (PAIR) {
+        if (lane == 0) arrive_even(bar(kHand + grp));
+        __syncwarp();
+        if (rank) return false;
+        waits(kHand + grp, (uint32_t)handed & 1u);
+        ++handed;
+      }
+      tc_fence_after();
+      return true;
+    };
     // NQ = 2: the groups take turns with the exponentials.  Both at once would share the unit for
     // them, finish together and then share the tensor cores; in turns, one's products run during the
     // other's exponentials.
@@ -241,7 +285,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     auto your_turn = [&] { asm volatile("bar.arrive %0, 256;" ::"r"(6 - grp) : "memory"); };
     if (NQ == 2 && grp == 1) your_turn();
     // products of the group, issued by one lane of its first warp
-    const uint32_t idc = idesc_f16(128);
+    const uint32_t idc = PAIR ? idesc_f16_pair(128) : idesc_f16(128);
+    auto mma = [&](uint32_t d, uint64_t x, uint64_t y, uint32_t acc) {
+      PAIR ? tc_mma_pair(d, x, y, idc, acc) : tc_mma(d, x, y, idc, acc);
+    };
+    auto bstep = [](uint32_t ks) { return (uint64_t)(((ks >> 2) * M::atom + (ks & 3) * 32) >> 4); };
     const uint32_t d_s = tmem + 128u * grp, d_o = tmem + 256u + 128u * grp;
     auto rotate = [&](uint32_t x, bool more, bool with_lo) {
       // scores (+)= x . (hi + lo)^T of the image (with_lo), or x . hi^T
@@ -250,23 +298,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       for (int part = 0; part < (with_lo ? 2 : 1); ++part)
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          tc_mma(d_s, dx + kstep(ks), di + kstep(ks) + part * (32768 >> 4), idc, more || (part | ks) != 0);
+          mma(d_s, dx + kstep(ks), di + bstep(ks) + part * (2 * M::atom >> 4), more || (part | ks) != 0);
     };
     auto scores = [&](int j) {
-      const uint64_t dq = smem_desc(sb + M::qhi + tile * kQHi), dk = smem_desc(sb + M::k + (j & 1) * kKBuf);
+      const uint32_t kb = sb + M::k + (j & 1) * M::kbuf;
+      const uint64_t dq = smem_desc(sb + M::qhi + tile * kQHi), dk = smem_desc(kb);
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks) tc_mma(d_s, dq + kstep(ks), dk + kstep(ks), idc, ks != 0);
-      tc_mma(d_s, smem_desc_plain(sb + M::qlo + tile * kQLo, 128, 256), dk, idc, 1);
-      tc_mma(d_s, dq, smem_desc_plain(sb + M::k + (j & 1) * kKBuf + 32768, 128, 256), idc, 1);
-      tc_commit(bar(kSFull + grp));
-      tc_commit(bar(kKEmpty + (j & 1)));
+      for (int ks = 0; ks < 8; ++ks) mma(d_s, dq + kstep(ks), dk + bstep(ks), ks != 0);
+      mma(d_s, smem_desc_plain(sb + M::qlo + tile * kQLo, 128, 256), dk, 1);
+      mma(d_s, dq, smem_desc_plain(kb + M::klo, 128, 256), 1);
+      commit(kSFull + grp);
+      commit(kKEmpty + (j & 1));
     };
     auto outputs = [&](int j, bool more) {
-      const uint64_t dv = smem_desc(sb + M::v + (j & 1) * 2 * kVAtom);
+      const uint64_t dv = smem_desc(sb + M::v + (j & 1) * 2 * M::atom);
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks)
-        tc_mma_ta(d_o, d_s + 8u * ks, dv + (uint64_t)(((ks >> 2) * kVAtom + (ks & 3) * 32) >> 4), idc, more || ks != 0);
-      tc_commit(bar(kVEmpty + (j & 1)));
+        PAIR ? tc_mma_ta_pair(d_o, d_s + 8u * ks, dv + bstep(ks), idc, more || ks != 0)
+             : tc_mma_ta(d_o, d_s + 8u * ks, dv + bstep(ks), idc, more || ks != 0);
+      commit(kVEmpty + (j & 1));
     };
     const int first = NQ == 2 ? 0 : grp, stride = NQ == 2 ? 1 : 2;  // the group's steps
     // raw queries -> operand, rotated by the tensor cores, back as scaled hi + lo
@@ -275,13 +325,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       put_query_row(sm + M::qhi + tile * kQHi, lrow,
                     reinterpret_cast<const uint4*>(a.q + b * a.qs[0] + hq * a.qs[1] + tok * a.qs[2]), mine);
       fence_async();
-      group_sync();
-      if (issuer) {
-        waits(kImg, 0);
-        tc_fence_after();
+      if (hand(0)) {
         if (elect_one() && !failed) {
           rotate(M::qhi + tile * kQHi, false, true);
-          tc_commit(bar(kQRot));
+          commit(kQRot);
         }
         __syncwarp();
       }
@@ -305,15 +352,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       tc_fence_before();
       fence_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kQFull));
+      if (!PAIR && lane == 0) mbar_arrive(bar(kQFull));
     }
     // steps
     int64_t end = !mine ? 0 : (a.causal ? len - cl + tok + 1 : len);  // tokens this row sees
     if (end > s1) end = s1;
     float ref = -INFINITY, sum = 0.f;
     int it = 0;
-    if (issuer && first < nb) {  // the first scores
-      waits(kQFull, 0);
+    if (PAIR ? hand(-1) : issuer && first < nb) {  // the first scores
+      if (!PAIR) waits(kQFull, 0);
       waits(kKFull + (first & 1), 0);
       tc_fence_after();
       if (elect_one() && !failed) scores(first);
@@ -355,8 +402,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       }
       if (NQ == 2 && (grp == 0 || j + 1 < nb)) your_turn();
       tc_fence_before();
-      group_sync();
-      if (issuer) {
+      if (hand(-1)) {
         waits(kVFull + (j & 1), (j >> 1) & 1);
         tc_fence_after();
         const int nj = j + stride;
@@ -370,14 +416,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         }
       }
     }
-    if (issuer && elect_one()) tc_commit(bar(kOFull));
+    if (issuer && rank == 0 && elect_one()) commit(kOFull);
     __syncwarp();
     // outputs: normalised, split into hi + lo operands of the last product
     waits(kOFull, 0);
     tc_fence_after();
     if (warp == 0 && lane == 0 && !failed) {  // the operands' memory is free: the values' rotation
-      mbar_expect_tx(bar(kImg), kImage);
-      bulk_load(sb + M::image, a.img_vt, kImage, bar(kImg));
+      load_image(a.img_vt);
     }
     __syncwarp();
     float total = sum, top = ref, other = 0.f;
@@ -436,14 +481,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       }
       tc_fence_before();
       fence_async();
-      group_sync();
-      if (issuer) {
-        waits(kImg, 1);
-        tc_fence_after();
+      if (hand(1)) {
         if (elect_one() && !failed) {
           rotate(M::qhi + tile * kQHi, false, true);
           rotate(M::olo + tile * 32768, true, false);
-          tc_commit(bar(kQRot));
+          commit(kQRot);
         }
         __syncwarp();
       }
@@ -487,49 +529,55 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       reinterpret_cast<uint32_t*>(&ms.m)[i] = reinterpret_cast<const uint32_t*>(a.meta + head)[i];
     load_dequant_tables(sm + M::tab, a.dec_image, dtid, 32 * kDqWarps);
     asm volatile("bar.sync 4, %0;" ::"n"(32 * kDqWarps) : "memory");
-    // quads dw and 15 - dw of the keys, dims 16 dw .. of the values, of every tile
+    // Keys: quads dw and 15 - dw of both tiles of a step, or (pairs) of this CTA's one, whose tokens
+    // are its half of the operand's rows.  Values: 16 dims of both tiles, or (pairs) of one of them,
+    // among this CTA's 64 dims.
+    constexpr int KT = PAIR ? 1 : 2;
     const uint32_t norms = key_norm_offset(a.kb, a.vb);
-    const KeyLane k0 = key_lane(ms.m, dw, lane, 16384, norms, tab);
-    const KeyLane k1 = key_lane(ms.m, 15 - dw, lane, 16384, norms, tab);
+    const KeyLane k0 = key_lane(ms.m, dw, lane, M::atom, norms, tab);
+    const KeyLane k1 = key_lane(ms.m, 15 - dw, lane, M::atom, norms, tab);
     const bool low = dw < kSplitSlots / 4;  // slots of quad dw leave low parts
     const bool code0 = low || __any_sync(0xffffffffu, k0.w > 4), code1 = __any_sync(0xffffffffu, k1.w > 4);
     const uint32_t lo_lane = (uint32_t)dw * 128 + 16u * (lane & 7) + 4u * (lane >> 3);
-    // addresses of a step's tiles: page numbers are read a step ahead of their use
+    const int vstep = PAIR ? 4 * rank + (dw & 3) : dw;
+    auto key_tile = [&](int j, int i) { return 2 * j + (PAIR ? rank : i); };
+    auto value_tile = [&](int j, int i) { return 2 * j + (PAIR ? dw >> 2 : i); };
+    // addresses: page numbers are read a step ahead of their use
     const int64_t t0 = s0 / kTile;
     const uint8_t* const base = a.packed + (a.sm.table ? (int64_t)h * a.sm.tile_bytes
                                                        : ((int64_t)head * a.sm.n_tiles + t0) * a.sm.tile_bytes);
     const int32_t* const pages = a.sm.table ? a.sm.table + (int64_t)b * a.sm.max_blocks + t0 : nullptr;
-    int page[2] = {0, 0};
-    auto read_pages = [&](int j) {
-      if (pages)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (2 * j + i < nt) page[i] = __ldg(pages + 2 * j + i);
+    auto read_page = [&](int t, int& page) {
+      if (pages && t < nt) page = __ldg(pages + t);
     };
-    auto tile_of = [&](int j, int i) {
-      return base + (pages ? (int64_t)page[i] * a.sm.hkv : (int64_t)(2 * j + i)) * a.sm.tile_bytes;
+    auto tile_of = [&](int t, int page) {
+      return base + (pages ? (int64_t)page * a.sm.hkv : (int64_t)t) * a.sm.tile_bytes;
     };
-    const uint8_t *kp[2], *vp[2];  // tiles of the keys in flight, and of the values due
-    KeyRaw r0[2], r1[2];
-    ValueRaw rv[2];
+    int kpage[KT] = {}, vpage[KT] = {};
+    const uint8_t *kp[KT], *vp[KT];
+    KeyRaw r0[KT], r1[KT];
+    ValueRaw rv[KT];
     auto fetch_keys = [&](int j) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        kp[i] = tile_of(j, i);
-        if (2 * j + i >= nt) break;
-        if (code0) load_keys<5>(r0[i], kp[i], k0);
-        else load_keys<2>(r0[i], kp[i], k0);
-        if (!code1) load_keys<2>(r1[i], kp[i], k1);
+      for (int i = 0; i < KT; ++i) {
+        const int t = key_tile(j, i);
+        if (t < nt) {
+          kp[i] = tile_of(t, kpage[i]);
+          if (code0) load_keys<5>(r0[i], kp[i], k0);
+          else load_keys<2>(r0[i], kp[i], k0);
+          if (!code1) load_keys<2>(r1[i], kp[i], k1);
+        }
+        read_page(key_tile(j + 1, i), kpage[i]);
       }
-      read_pages(j + 1);
     };
     auto put_keys = [&](int j) {
-      const uint32_t dst = sb + M::k + (j & 1) * kKBuf;
+      const uint32_t dst = sb + M::k + (j & 1) * M::kbuf;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (2 * j + i >= nt) break;  // rows behind the last tile: whatever they hold, their scores do not count
+      for (int i = 0; i < KT; ++i) {
+        // rows behind the last tile: whatever they hold, their scores do not count
+        if (key_tile(j, i) >= nt) continue;
         const uint32_t row = dst + i * 8192;
-        if (code0) keys_by_code(k0, r0[i], tab, row, low, dst + 32768 + i * 2048 + lo_lane, 256);
+        if (code0) keys_by_code(k0, r0[i], tab, row, low, dst + M::klo + i * 2048 + lo_lane, 256);
         else keys_by_pair(k0, r0[i], row);
         if (!code1) {
           keys_by_pair(k1, r1[i], row);
@@ -540,18 +588,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         }
       }
     };
-    read_pages(0);
+    auto arrive = [&](int i) { PAIR ? arrive_even(bar(i)) : mbar_arrive(bar(i)); };
+#pragma unroll
+    for (int i = 0; i < KT; ++i) {
+      read_page(key_tile(0, i), kpage[i]);
+      read_page(value_tile(0, i), vpage[i]);
+    }
     fetch_keys(0);
     // the keys' buffers lie under the rotation image
-    if (!mbar_wait(bar(kQRot), 0)) failed = 1;
+    if (!wait_on(kQRot, 0)) failed = 1;
     __syncwarp();
     if (!failed) {
       put_keys(0);
       fence_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kKFull));
-      vp[0] = kp[0];
-      vp[1] = kp[1];
+      if (lane == 0) arrive(kKFull);
       if (nb > 1) fetch_keys(1);
     }
     // step by step: the keys of step j + 1, then the values of step j (a fence costs as much as
@@ -559,48 +610,53 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
 #pragma unroll 1
     for (int j = 0; j < nb && !failed; ++j) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (2 * j + i < nt) load_values(rv[i], vp[i], a.kb, a.vb, dw, lane);
+      for (int i = 0; i < KT; ++i) {
+        const int t = value_tile(j, i);
+        if (t < nt) {
+          vp[i] = tile_of(t, vpage[i]);
+          load_values(rv[i], vp[i], a.kb, a.vb, vstep, lane);
+        }
+        read_page(value_tile(j + 1, i), vpage[i]);
+      }
       if (j + 1 < nb) {
-        if (j >= 1 && !mbar_wait(bar(kKEmpty + ((j + 1) & 1)), (((j + 1) >> 1) & 1) ^ 1)) { failed = 1; break; }
+        if (j >= 1 && !wait_on(kKEmpty + ((j + 1) & 1), (((j + 1) >> 1) & 1) ^ 1)) { failed = 1; break; }
         __syncwarp();
         put_keys(j + 1);
       }
-      const uint8_t *n0 = kp[0], *n1 = kp[1];
       if (j + 2 < nb) fetch_keys(j + 2);  // in flight during the values
-      // and what is due two steps later, towards the L2 cache (the warps take turns)
+      // and what is due two steps later, towards the L2 cache (the warps take turns; a pair's CTAs a
+      // tile each)
       if (lane == 0 && (j & 7) == dw)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int t = 2 * (j + 4) + i;
+        for (int i = 0; i < KT; ++i) {
+          const int t = key_tile(j + 4, i);
           if (t < nt)
             bulk_prefetch(base + (pages ? (int64_t)__ldg(pages + t) * a.sm.hkv : (int64_t)t) * a.sm.tile_bytes,
                           (uint32_t)a.sm.tile_bytes);
         }
-      if (j >= 2 && !mbar_wait(bar(kVEmpty + (j & 1)), ((j >> 1) & 1) ^ 1)) { failed = 1; break; }
+      if (j >= 2 && !wait_on(kVEmpty + (j & 1), ((j >> 1) & 1) ^ 1)) { failed = 1; break; }
       __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int v = 2 * j + i;
-        const uint32_t atom = M::v + (2 * (j & 1) + i) * kVAtom;
-        if (v < nt) {
-          const int64_t left = s1 - (s0 + (int64_t)v * kTile);
+      for (int i = 0; i < KT; ++i) {
+        const int t = value_tile(j, i);
+        const uint32_t atom = M::v + (2 * (j & 1) + (t & 1)) * M::atom;
+        const uint32_t first_row = PAIR ? (uint32_t)rank * 8192u : 0u;  // dim 16 vstep lies 2048 vstep behind dim 0
+        if (t < nt) {
+          const int64_t left = s1 - (s0 + (int64_t)t * kTile);
           uint32_t n[8];
           value_norms(rv[i], lane, left < kTile ? (int)left : kTile, n);
-          dequant_values(vp[i], a.kb, a.vb, dw, lane, rv[i], n, tab, sb + atom);
+          dequant_values(vp[i], a.kb, a.vb, vstep, lane, rv[i], n, tab, sb + atom - first_row);
         } else {  // no tile: zeros, since the probabilities' zeros must not meet a NaN
           for (int k = lane; k < 128; k += 32)
-            *reinterpret_cast<uint4*>(sm + atom + dw * 2048 + 16 * k) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(sm + atom - first_row + vstep * 2048 + 16 * k) = make_uint4(0, 0, 0, 0);
         }
       }
       fence_async();
       __syncwarp();
       if (lane == 0) {
-        if (j + 1 < nb) mbar_arrive(bar(kKFull + ((j + 1) & 1)));
-        mbar_arrive(bar(kVFull + (j & 1)));
+        if (j + 1 < nb) arrive(kKFull + ((j + 1) & 1));
+        arrive(kVFull + (j & 1));
       }
-      vp[0] = n0;
-      vp[1] = n1;
     }
   }
   if (failed) atomicOr(a.status, kStatusTimeout);
@@ -609,8 +665,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
   if (__syncthreads_or(failed)) {
     if (warp == 0 || warp == 4) {
       if (elect_one()) {  // the lane that issued them
-        tc_commit(bar(kDrain + (warp >> 2)));
-        mbar_wait(bar(kDrain + (warp >> 2)), 0);
+        if (rank == 0) commit(kDrain + (warp >> 2));
+        wait_on(kDrain + (warp >> 2), 0);
       }
     }
     if (tid == 0) {
@@ -620,7 +676,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  if (PAIR) {
+    cluster_sync_all();  // nothing of the other CTA is touched past this point
+    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  } else if (warp == 0) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
 }
 
 // The splits' outputs of a row, weighted by what their maxima and sums say.  WPR warps a row: one
@@ -738,38 +799,41 @@ cudaError_t launch_token(const gtq_plan* p, const uint8_t* packed, int64_t T, co
 
 // How a call is cut: rows per block and splits of the tokens.
 struct Cut {
-  int nq, row_tiles, splits;
+  int nq, pair, row_tiles, splits;
   int64_t span, rows_pad;
   uint32_t smem;
 };
 
-template <int NQ>
+template <int NQ, bool PAIR>
 constexpr uint32_t smem_of() {
-  return Map<NQ>::misc + (uint32_t)sizeof(Misc);
+  return Map<NQ, PAIR>::misc + (uint32_t)sizeof(Misc);
 }
-static_assert(smem_of<2>() <= 232448, "shared memory of a block");
+static_assert(smem_of<2, false>() <= 232448 && smem_of<2, true>() <= 232448, "shared memory of a block");
 
 Cut cut_of(const gtq_plan* p, int64_t T, int64_t n) {
   Cut c;
   const int64_t rows = n * p->g_q;
   c.nq = rows > 128 ? 2 : 1;
-  c.smem = c.nq == 2 ? smem_of<2>() : smem_of<1>();
-  c.row_tiles = (int)((rows + 128 * c.nq - 1) / (128 * c.nq));
-  c.rows_pad = (int64_t)c.row_tiles * 128 * c.nq;
-  // Splits: enough blocks to fill the SMs, and evenly; a block's set-up and end cost about as
-  // much as 8 steps, a merge more the more parts there are.
+  c.pair = rows > 256;
+  c.smem = c.pair ? smem_of<2, true>() : (c.nq == 2 ? smem_of<2, false>() : smem_of<1, false>());
+  const int64_t unit = 128 * c.nq * (c.pair ? 2 : 1);
+  c.row_tiles = (int)((rows + unit - 1) / unit);
+  c.rows_pad = (int64_t)c.row_tiles * unit;
+  // Splits: enough blocks (pairs) to fill the SMs, and evenly; a block's set-up and end cost about
+  // as much as 6 steps, a merge more the more parts there are.
   const int64_t units = (int64_t)p->n_heads * c.row_tiles, steps = (T + kBlockTok - 1) / kBlockTok;
+  const int64_t at_once = c.pair ? p->n_sms / 2 : p->n_sms;
   double best = 1e300;
   int64_t best_steps = steps;
   for (int64_t s = 1; s <= 256 && s <= steps; ++s) {
     const int64_t per = (steps + s - 1) / s, parts = (steps + per - 1) / per;
-    const int64_t waves = (units * parts + p->n_sms - 1) / p->n_sms;
-    const double cost = (double)waves * (per + 8.0) + (parts > 1 ? 4.0 + 0.02 * parts * units / p->n_sms : 0.0);
+    const int64_t waves = (units * parts + at_once - 1) / at_once;
+    const double cost = (double)waves * (per + 6.0) + (parts > 1 ? 2.0 + 0.01 * parts * c.rows_pad * p->n_heads / 256 / p->n_sms : 0.0);
     if (cost < best * 0.999) {
       best = cost;
       best_steps = per;
     }
-    if (units * s > 64 * (int64_t)p->n_sms) break;
+    if (units * s > 64 * at_once) break;
   }
   c.span = best_steps * kBlockTok;
   c.splits = (int)((steps + best_steps - 1) / best_steps);
@@ -821,11 +885,22 @@ cudaError_t launch_chunk(const gtq_plan* p, const uint8_t* packed, int64_t T, co
   const size_t slots = (size_t)p->n_heads * c.splits * c.rows_pad;
   a.part_o = reinterpret_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(workspace + slots * kD * sizeof(float));
-  auto kernel = c.nq == 2 ? chunk_kernel<2> : chunk_kernel<1>;
+  auto kernel = c.pair ? chunk_kernel<2, true> : (c.nq == 2 ? chunk_kernel<2, false> : chunk_kernel<1, false>);
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)c.smem);
   if (e != cudaSuccess) return e;
-  kernel<<<dim3((unsigned)(c.row_tiles * c.splits), (unsigned)p->n_heads), kChunkThreads, c.smem, s>>>(a);
-  e = cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(c.row_tiles * c.splits * (c.pair ? 2 : 1)), (unsigned)p->n_heads);
+  cfg.blockDim = dim3(kChunkThreads);
+  cfg.dynamicSmemBytes = c.smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = c.pair ? 2 : 1;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, a);
   if (e != cudaSuccess || c.splits == 1) return e;
   const int64_t rows = ch.n_tokens * p->g_q;
   if (c.splits >= 8)
