@@ -78,9 +78,9 @@ struct Misc {
 };
 
 // barriers
-constexpr int kKFull = 0;           // [2] keys of a step written
+constexpr int kK0Full = 0;          // keys of the first step written
 constexpr int kKEmpty = 2;          // [2] their products done
-constexpr int kVFull = 4;           // [2] values of a step written
+constexpr int kFull = 4;            // [2] values of a step and keys of the next written
 constexpr int kVEmpty = 6;          // [2] their products done
 constexpr int kSFull = 8;           // [2] scores written
 constexpr int kImg = 10;            // rotation image landed
@@ -209,14 +209,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
   // ---------------------------------------------------------------- set-up
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(kKFull + i), kDqWarps * (PAIR ? 2 : 1));
       mbar_init(bar(kHand + i), 2);
       mbar_init(bar(kKEmpty + i), NQ);
-      mbar_init(bar(kVFull + i), kDqWarps * (PAIR ? 2 : 1));
+      mbar_init(bar(kFull + i), kDqWarps * (PAIR ? 2 : 1));
       mbar_init(bar(kVEmpty + i), NQ);
       mbar_init(bar(kSFull + i), 1);
       mbar_init(bar(kDrain + i), 1);
     }
+    mbar_init(bar(kK0Full), kDqWarps * (PAIR ? 2 : 1));
     mbar_init(bar(kImg), 1);
     mbar_init(bar(kQRot), NQ);
     mbar_init(bar(kQFull), 4 * NQ);
@@ -355,13 +355,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       if (!PAIR && lane == 0) mbar_arrive(bar(kQFull));
     }
     // steps
-    int64_t end = !mine ? 0 : (a.causal ? len - cl + tok + 1 : len);  // tokens this row sees
+    // tokens this row sees; a row that is not there (zeros, its result goes nowhere) keeps its warp
+    // from masking by seeing whole steps
+    int64_t end = a.causal ? len - cl + tok + 1 : len;
     if (end > s1) end = s1;
+    if (!mine) end = s0 + (int64_t)nb * kBlockTok;
     float ref = -INFINITY, sum = 0.f;
     int it = 0;
     if (PAIR ? hand(-1) : issuer && first < nb) {  // the first scores
       if (!PAIR) waits(kQFull, 0);
-      waits(kKFull + (first & 1), 0);
+      if (first == 0) waits(kK0Full, 0);
+      else waits(kFull, 0);
       tc_fence_after();
       if (elect_one() && !failed) scores(first);
       __syncwarp();
@@ -403,13 +407,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       if (NQ == 2 && (grp == 0 || j + 1 < nb)) your_turn();
       tc_fence_before();
       if (hand(-1)) {
-        waits(kVFull + (j & 1), (j >> 1) & 1);
+        waits(kFull + (j & 1), (j >> 1) & 1);
         tc_fence_after();
         const int nj = j + stride;
-        if (elect_one() && !failed) outputs(j, it > 0);
+        if (elect_one() && !failed) {
+          outputs(j, it > 0);
+          if (NQ == 2 && nj < nb) scores(nj);
+        }
         __syncwarp();
-        if (nj < nb) {
-          waits(kKFull + (nj & 1), (nj >> 1) & 1);
+        if (NQ == 1 && nj < nb) {  // its keys come with the other group's values
+          waits(kFull + ((j + 1) & 1), ((j + 1) >> 1) & 1);
           tc_fence_after();
           if (elect_one() && !failed) scores(nj);
           __syncwarp();
@@ -602,7 +609,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       put_keys(0);
       fence_async();
       __syncwarp();
-      if (lane == 0) arrive(kKFull);
+      if (lane == 0) arrive(kK0Full);
       if (nb > 1) fetch_keys(1);
     }
     // step by step: the keys of step j + 1, then the values of step j (a fence costs as much as
@@ -653,10 +660,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       }
       fence_async();
       __syncwarp();
-      if (lane == 0) {
-        if (j + 1 < nb) arrive(kKFull + ((j + 1) & 1));
-        arrive(kVFull + (j & 1));
-      }
+      if (lane == 0) arrive(kFull + (j & 1));
     }
   }
   if (failed) atomicOr(a.status, kStatusTimeout);
