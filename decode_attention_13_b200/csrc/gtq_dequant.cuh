@@ -56,6 +56,21 @@ __device__ __forceinline__ void load_dequant_tables(uint8_t* tab, const uint4* i
   if (tid < 32) reinterpret_cast<uint32_t*>(tab + kDqZero)[tid] = 0;
 }
 
+// The low parts of the pair tables, laid out as the tables themselves (their single codes left out).
+__device__ __forceinline__ void load_dequant_tables_lo(uint8_t* tab, const uint4* image, int tid, int n_threads) {
+  const uint32_t* ss = reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(image) + kTabSS);
+  auto pair = [&](int w, int i) {
+    const uint32_t* e = ss + kSingleOff(w) / 4;
+    return as_u32(__hmul2(as_h2(__byte_perm(e[i & ((1 << w) - 1)], e[i >> w], 0x7632)), __float2half2_rn(0.0625f)));
+  };
+#pragma unroll
+  for (int w = 1; w <= 3; ++w)
+    for (int i = tid; i < (32 << (2 * w)); i += n_threads)
+      reinterpret_cast<uint32_t*>(tab + kDqPairs + (kTabP32(w) - kTabP32W3))[i] = pair(w, i >> 5);
+  for (int i = tid; i < 256; i += n_threads) reinterpret_cast<uint32_t*>(tab + kDqPair4)[i] = pair(4, i);
+  if (tid < 32) reinterpret_cast<uint32_t*>(tab + kDqZero)[tid] = 0;
+}
+
 // From the lookup tables, which never change: the compiler may move it anywhere.
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
@@ -174,6 +189,36 @@ __device__ __forceinline__ void keys_by_pair(const KeyLane& k, const KeyRaw& r, 
     const __half2 n = as_h2(nw[u >> 1]);
     sts32(d + 1024 * u, as_u32(__hmul2(as_h2(v[u]), __low2half2(n))));
     sts32(d + 1024 * (u + 1), as_u32(__hmul2(as_h2(v[u + 1]), __high2half2(n))));
+  }
+}
+
+// The same with the products' rests beyond fp16 (fp16 hi + lo of the codebook in two tables `lo_tab`
+// bytes apart), `lo_dst` bytes behind the pair itself.
+__device__ __forceinline__ void keys_by_pair_split(const KeyLane& k, const KeyRaw& r, uint32_t dst,
+                                                   uint32_t lo_tab, uint32_t lo_dst) {
+  const uint32_t w2 = 2 * k.w, odd = (k.src & 2u) * 8u, mask = (1u << w2) - 1;
+  uint32_t x[2];
+  x[0] = __funnelshift_r(r.x[0], r.x[1], odd);
+  x[1] = __funnelshift_rc(x[0], r.x[1] >> odd, 4 * w2);
+  const uint32_t nw[4] = {r.n.x, r.n.y, r.n.z, r.n.w};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t v[4], l[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t at = (x[i] & mask) * k.step + k.base;
+      v[u] = lds32(at);
+      l[u] = lds32(at + lo_tab);
+      x[i] >>= w2;
+    }
+    const uint32_t d = dst + k.col + 4096 * i;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const __half2 n = as_h2(nw[2 * i + (u >> 1)]), nn = (u & 1) ? __high2half2(n) : __low2half2(n);
+      const __half2 p = __hmul2(as_h2(v[u]), nn);
+      sts32(d + 1024 * u, as_u32(p));
+      sts32(d + 1024 * u + lo_dst, as_u32(__hfma2(as_h2(l[u]), nn, __hfma2(as_h2(v[u]), nn, __hneg2(p)))));
+    }
   }
 }
 

@@ -35,14 +35,14 @@ constexpr int kThreadsW = 32 * (kReadWarps + kDqWarps);
 constexpr int kStepTok = 128;
 constexpr int kRowsW = 128;
 constexpr int kKeepRows = 64;  // rows whose scores are kept (8 bytes moved a row and token against about 1000 for pass 1)
-constexpr int kAheadW = 6;  // packed tiles between a prefetch and its use
+constexpr int kAheadW = 8;   // packed tiles between a prefetch and its use
 
 // shared memory: queries and two steps of keys, each fp16 hi and lo (two swizzled atoms a part)
 constexpr uint32_t kPart = 32768;
 constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffK = 2 * kPart;
 constexpr uint32_t kOffTab = kOffK + 4 * kPart;
-constexpr uint32_t kOffMisc = kOffTab + kDqBytes;
+constexpr uint32_t kOffMisc = kOffTab + 2 * kDqBytes;  // pair tables, then their low parts
 constexpr uint32_t kImageBytes = 65536;  // the keys' rotation, under the keys until the queries are turned
 struct MiscW {
   alignas(16) HeadMeta m;
@@ -259,9 +259,11 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
     }
     // pass 0: the row on this lane
     int64_t end = 0;
-    if (PASS == 0 && lrow < rows) {
+    if (PASS == 0) {
       end = a.causal ? len - cl + ((int)r0 + lrow) / a.gq + 1 : len;
       if (end > s1) end = s1;
+      // a row that is not there keeps its warp from masking by seeing whole steps
+      if (lrow >= rows) end = s0 + (int64_t)nb * kStepTok;
     }
     const int64_t first_end = len - cl + (int)r0 / a.gq;  // last token that the first row sees
     const bool warp_on = PASS == 1 || (warp & 3) * 32 < rows;
@@ -356,6 +358,7 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
     for (int i = dtid; i < (int)(sizeof(HeadMeta) / 4); i += 32 * kDqWarps)
       reinterpret_cast<uint32_t*>(&ms.m)[i] = reinterpret_cast<const uint32_t*>(a.meta + head)[i];
     load_dequant_tables(sm + kOffTab, a.dec_image, dtid, 32 * kDqWarps);
+    load_dequant_tables_lo(sm + kOffTab + kDqBytes, a.dec_image, dtid, 32 * kDqWarps);
     asm volatile("bar.sync 4, %0;" ::"n"(32 * kDqWarps) : "memory");
     const uint32_t tab = sb + kOffTab, norms = key_norm_offset(a.kb, a.vb);
     const KeyLane k0 = key_lane(ms.m, dw, lane, 16384, norms, tab), k1 = key_lane(ms.m, 15 - dw, lane, 16384, norms, tab);
@@ -363,41 +366,57 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
     const uint8_t* const base = a.packed + (a.sm.table ? (int64_t)h * a.sm.tile_bytes
                                                        : ((int64_t)head * a.sm.n_tiles + t0) * a.sm.tile_bytes);
     const int32_t* const pages = a.sm.table ? a.sm.table + (int64_t)b * a.sm.max_blocks + t0 : nullptr;
-    auto tile_at = [&](int t) {
-      return base + (pages ? (int64_t)__ldg(pages + t) * a.sm.hkv : (int64_t)t) * a.sm.tile_bytes;
+    const bool code0 = __any_sync(0xffffffffu, k0.w > 4), code1 = __any_sync(0xffffffffu, k1.w > 4);
+    // a set of registers for each tile of a step: a tile's set is filled again as soon as it is
+    // used, a whole step before it is due
+    KeyRaw r0k[2], r1k[2];
+    int page[2] = {0, 0};
+    auto read_page = [&](int t) {
+      if (pages && t < nt) page[t & 1] = __ldg(pages + t);
     };
-    KeyRaw r0k, r1k;
-    auto fetch = [&](const uint8_t* p) {
-      load_keys<5>(r0k, p, k0);
-      load_keys<5>(r1k, p, k1);
+    auto fetch = [&](int t, int i) {
+      if (t < nt) {
+        const uint8_t* p = base + (pages ? (int64_t)page[i] * a.sm.hkv : (int64_t)t) * a.sm.tile_bytes;
+        if (code0) load_keys<5>(r0k[i], p, k0);
+        else load_keys<2>(r0k[i], p, k0);
+        if (code1) load_keys<5>(r1k[i], p, k1);
+        else load_keys<2>(r1k[i], p, k1);
+      }
     };
-    fetch(tile_at(0));
-    const uint8_t* next = nt > 1 ? tile_at(1) : nullptr;
+    read_page(0);
+    read_page(1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      fetch(i, i);
+      read_page(2 + i);
+    }
     if (!mbar_wait(bar(kQRot), 0)) failed = 1;  // the keys' buffers lie under the rotation image
     __syncwarp();
 #pragma unroll 1
-    for (int t = 0; t < 2 * nb && !failed; ++t) {
-      const int j = t >> 1;
-      if (!(t & 1) && j >= 2 && !mbar_wait(bar(kKEmpty + (j & 1)), ((j >> 1) & 1) ^ 1)) { failed = 1; break; }
+    for (int j = 0; j < nb && !failed; ++j) {
+      if (j >= 2 && !mbar_wait(bar(kKEmpty + (j & 1)), ((j >> 1) & 1) ^ 1)) { failed = 1; break; }
       __syncwarp();
-      if (t < nt) {
-        const KeyRaw c0 = r0k, c1 = r1k;
-        if (next) fetch(next);  // in flight during this tile
-        next = t + 2 < nt ? tile_at(t + 2) : nullptr;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int t = 2 * j + i;
+        if (t >= nt) break;
+        const uint32_t row = sb + kOffK + (j & 1) * 2 * kPart + i * 8192;
+        if (code0) keys_by_code(k0, r0k[i], tab, row, true, row + kPart + k0.col, 1024);
+        else keys_by_pair_split(k0, r0k[i], row, kDqBytes, kPart);
+        if (code1) keys_by_code(k1, r1k[i], tab, row, true, row + kPart + k1.col, 1024);
+        else keys_by_pair_split(k1, r1k[i], row, kDqBytes, kPart);
+        fetch(t + 2, i);
+        read_page(t + 4);
         if (t + kAheadW < nt && lane == 0 && (t & 7) == dw) {  // towards the L2 cache (the warps take turns)
-          const uint8_t* p = tile_at(t + kAheadW);
+          const uint8_t* p = base + (pages ? (int64_t)__ldg(pages + t + kAheadW) * a.sm.hkv
+                                           : (int64_t)(t + kAheadW)) * a.sm.tile_bytes;
           bulk_prefetch(p, 1024u * a.kb);
           bulk_prefetch(p + norms, 1024u);
         }
-        const uint32_t row = sb + kOffK + (j & 1) * 2 * kPart + (t & 1) * 8192;
-        keys_by_code(k0, c0, tab, row, true, row + kPart + k0.col, 1024);
-        keys_by_code(k1, c1, tab, row, true, row + kPart + k1.col, 1024);
       }
-      if (t & 1) {
-        fence_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kKFull + (j & 1)));
-      }
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kKFull + (j & 1)));
     }
   }
   if (failed) atomicOr(a.status, kStatusTimeout);
