@@ -15,8 +15,9 @@
 // products of fp16 halves carry about 22 bits of each factor.
 //
 // With up to kKeepRows rows of a KV head, pass 0 leaves the scores themselves (4 bytes a row
-// and token) and kept_kernel takes the place of pass 1: reading them again costs less than
-// turning the codes into operands again (8 rows over 2 x 131072 tokens: 41 us for pass 1).
+// and token) and kept_kernel takes the place of pass 1: writing and reading them costs less than
+// turning the codes into operands again (2 heads of 131072 tokens: 8 rows 50 us against 69, 16
+// rows 60 against 70, 24 rows 72 against 70, 64 rows 138 against 73).
 // Rows beyond 128 of a KV head are more blocks, whose sums lie side by side in the
 // workspace until add_kernel joins them in order.
 #include <algorithm>
@@ -34,7 +35,7 @@ constexpr int kDqWarps = 8;
 constexpr int kThreadsW = 32 * (kReadWarps + kDqWarps);
 constexpr int kStepTok = 128;
 constexpr int kRowsW = 128;
-constexpr int kKeepRows = 64;  // rows whose scores are kept (8 bytes moved a row and token against about 1000 for pass 1)
+constexpr int kKeepRows = 16;  // rows whose scores are kept
 constexpr int kAheadW = 8;   // packed tiles between a prefetch and its use
 
 // shared memory: queries and two steps of keys, each fp16 hi and lo (two swizzled atoms a part)
