@@ -345,8 +345,12 @@ int gtq_rope(const gtq_rope_config* cfg, int64_t batch, int64_t tokens, const in
     if (!t->x || !t->y || !aligned(t->x, es) || !aligned(t->y, es)) return GTQ_ERR_INVALID;
     if (t->heads < 1 || t->heads > 65535 || t->reserved != 0) return GTQ_ERR_INVALID;
     if (t->x_strides[3] != 1 || t->y_strides[3] != 1) return GTQ_ERR_INVALID;
-    for (int i = 0; i < 3; ++i)
+    const int64_t extent[3] = {batch, t->heads, tokens};
+    for (int i = 0; i < 3; ++i) {
       if (t->x_strides[i] < 0 || t->y_strides[i] < 0) return GTQ_ERR_INVALID;
+      if (extent[i] > 1 && t->y_strides[i] == 0) return GTQ_ERR_INVALID;
+      if (extent[i] > 1 && t->x == t->y && t->x_strides[i] != t->y_strides[i]) return GTQ_ERR_INVALID;
+    }
   }
   return cuda_code(launch_rope(c, batch, tokens, positions_dev, pos_stride, pos0, q, k,
                                (cudaStream_t)stream));
@@ -374,8 +378,13 @@ int gtq_chunk_attn(gtq_plan* plan, const void* packed_dev, int64_t T, const gtq_
   if (rc != GTQ_OK) return rc;
   if (plan->cfg.v_bits == 0) return GTQ_ERR_UNSUPPORTED;
   if (!out_dev || !aligned(out_dev, 16) || chunk->out_strides[3] != 1) return GTQ_ERR_INVALID;
-  for (int i = 0; i < 3; ++i)
+  const int64_t extent[3] = {plan->cfg.batch, plan->cfg.n_q_heads, chunk->n_tokens};
+  for (int i = 0; i < 3; ++i) {
     if (chunk->out_strides[i] < 0 || chunk->out_strides[i] % 8) return GTQ_ERR_INVALID;
+    if (extent[i] > 1 && chunk->out_strides[i] == 0) return GTQ_ERR_INVALID;
+    if (extent[i] > 1 && q_dev == out_dev && chunk->q_strides[i] != chunk->out_strides[i])
+      return GTQ_ERR_INVALID;
+  }
   if (workspace_bytes < chunk_workspace(plan, T, chunk->n_tokens)) return GTQ_ERR_INVALID;
   OnDevice on(plan->device);
   if (on.err != cudaSuccess) return cuda_code(on.err);
@@ -393,6 +402,8 @@ int gtq_attn_weights(gtq_plan* plan, const void* packed_dev, int64_t T, const gt
   if (!weights_out_dev || !w_strides || !aligned(weights_out_dev, 4) || !aligned(weights_in_dev, 4))
     return GTQ_ERR_INVALID;
   if (w_strides[0] < 0 || w_strides[1] < 0) return GTQ_ERR_INVALID;
+  if ((plan->cfg.batch > 1 && w_strides[0] == 0) || (plan->cfg.n_kv_heads > 1 && w_strides[1] == 0))
+    return GTQ_ERR_INVALID;
   if (workspace_bytes < weights_workspace(plan, T, chunk->n_tokens)) return GTQ_ERR_INVALID;
   OnDevice on(plan->device);
   if (on.err != cudaSuccess) return cuda_code(on.err);
@@ -414,9 +425,17 @@ int gtq_evict(gtq_plan* plan, const void* src_dev, int64_t T, const gtq_seq_layo
   if (!ev->weights_dev || !ev->new_lens_dev || !aligned(ev->weights_dev, 4) ||
       !aligned(ev->weights_out_dev, 4) || !aligned(ev->kept_dev, 4) || !aligned(ev->new_lens_dev, 4))
     return GTQ_ERR_INVALID;
-  for (int i = 0; i < 2; ++i)
-    if (ev->w_strides[i] < 0 || (ev->weights_out_dev && ev->w_out_strides[i] < 0))
+  const int64_t extent[2] = {plan->cfg.batch, plan->cfg.n_kv_heads};
+  for (int i = 0; i < 2; ++i) {
+    if (ev->w_strides[i] < 0) return GTQ_ERR_INVALID;
+    if (ev->weights_out_dev && (ev->w_out_strides[i] < 0 || (extent[i] > 1 && ev->w_out_strides[i] == 0)))
       return GTQ_ERR_INVALID;
+  }
+  // blocks read the old lengths and weights while others write the new ones
+  if (ev->weights_out_dev == ev->weights_dev) return GTQ_ERR_INVALID;
+  if (lay && lay->seq_lens_dev && ev->new_lens_dev < lay->seq_lens_dev + plan->cfg.batch &&
+      lay->seq_lens_dev < ev->new_lens_dev + plan->cfg.batch)
+    return GTQ_ERR_INVALID;
   if (!aligned(src_dev, 16) || !aligned(dst_dev, 16) || !aligned(workspace_dev, 256))
     return GTQ_ERR_INVALID;
   if (check_layout(lay, T) != GTQ_OK ||
@@ -425,6 +444,8 @@ int gtq_evict(gtq_plan* plan, const void* src_dev, int64_t T, const gtq_seq_layo
   const bool paged = lay && lay->block_table_dev, dst_paged = dst_lay && dst_lay->block_table_dev;
   const size_t need = dst_paged ? (size_t)plan->cfg.n_kv_heads * plan->tile_bytes : plan->packed_bytes;
   if (dst_bytes < need) return GTQ_ERR_INVALID;
+  if (paged && dst_paged && src_dev == dst_dev && lay->block_table_dev == dst_lay->block_table_dev)
+    return GTQ_ERR_INVALID;  // the same pages
   if (!paged && !dst_paged) {  // two contiguous caches: their ranges are known here
     const uintptr_t s = (uintptr_t)src_dev, d = (uintptr_t)dst_dev;
     if (s < d + plan->packed_bytes && d < s + plan->packed_bytes) return GTQ_ERR_INVALID;

@@ -324,8 +324,9 @@ typedef struct gtq_rope_config {
 
 /* One tensor of rows: x element (b, h, t, i) at x + b*x_strides[0] +
  * h*x_strides[1] + t*x_strides[2] + i (strides in elements, x_strides[3] must be
- * 1, none negative), y likewise.  y may be x with the same strides (in place);
- * any other overlap is not supported.  No alignment beyond the element's own. */
+ * 1, none negative), y likewise, without a 0 where the extent is above 1.  y may be
+ * x with the same strides (in place); any other overlap is not supported.  No
+ * alignment beyond the element's own. */
 typedef struct gtq_rope_tensor {
   const void* x;
   void* y;
@@ -363,7 +364,8 @@ GTQ_API int gtq_rope(const gtq_rope_config* cfg, int64_t batch, int64_t tokens,
  *   q_strides   strides of q in elements, element (b, hq, i, dim) at q + b*s[0] +
  *               hq*s[1] + i*s[2] + dim (s[3] must be 1, the others multiples of
  *               8 and not negative; q 16-byte aligned).
- *   out_strides the same for out (gtq_chunk_attn); rows must not overlap.
+ *   out_strides the same for out (gtq_chunk_attn); rows must not overlap (a stride
+ *               of 0 is refused where the extent is above 1).
  */
 typedef struct gtq_chunk {
   int64_t n_tokens;              /* rows per sequence at most, 1..2^20 */
@@ -382,12 +384,16 @@ typedef struct gtq_chunk {
  *   packed_dev, T, lay  as gtq_decode_attn_ex (contiguous or paged; lengths).
  *   q_dev     fp16 post-RoPE queries; query head hq uses KV head hq / (Hq / Hkv).
  *   out_dev   fp16, 16-byte aligned.  Rows i >= n_b are left as they are; a row
- *             that sees no token gets zeros.
+ *             that sees no token gets zeros.  out may be q with the same strides; any
+ *             other overlap is not supported.
  *   workspace_dev  workspace_bytes >= gtq_chunk_workspace_bytes(plan, T, n_tokens),
  *             256-byte aligned.  It holds nothing between calls; calls that may
  *             overlap (other streams, graphs replayed at once) need one each.
- * Keys are attended with the wide groups' products in split fp16 and the others
- * in fp16, as in gtq_decode_attn; scores, softmax statistics and sums are fp32.
+ * n_tokens 1 runs the kernel of gtq_decode_attn.  With more, a score's products are
+ * fp16 x fp16 in fp32, and those of the 16 coordinates with the widest codes carry
+ * the low parts of both factors as well; probabilities enter the second product as
+ * fp16; softmax statistics and sums are fp32.  A row with a NaN in its query gets
+ * NaNs (n_tokens above 1) and changes no other row.
  * Errors: INVALID, UNSUPPORTED (head_dim != 128; a K-only plan), CUDA.
  */
 GTQ_API int gtq_chunk_attn(gtq_plan* plan, const void* packed_dev, int64_t T,
@@ -404,10 +410,11 @@ GTQ_API size_t gtq_chunk_workspace_bytes(const gtq_plan* plan, int64_t T, int64_
  * (a row that sees no token adds nothing).  It is what gtq_evict chooses by.
  *   weights_in_dev   fp32, element (b, h, t) at b*w_strides[0] + h*w_strides[1] + t,
  *                    or NULL: zeros.  May be weights_out_dev.
- *   weights_out_dev  fp32, the same strides (not negative); elements t >= len_b are
- *                    left as they are.
+ *   weights_out_dev  fp32, the same strides (not negative, 0 only for an extent of 1);
+ *                    elements t >= len_b are left as they are.
  *   others           as gtq_chunk_attn (out_strides are not read);
- *                    workspace_bytes >= gtq_weights_workspace_bytes(...).
+ *                    workspace_bytes >= gtq_weights_workspace_bytes(...) (up to 16 rows
+ *                    of a KV head, it holds their fp32 scores).
  * Sums run in a fixed order: the same call gives the same bits.  Scores are
  * exact to about 2^-21 of the largest product.  K-only plans are supported.
  * Errors: INVALID, UNSUPPORTED (head_dim != 128), CUDA.
@@ -438,7 +445,8 @@ typedef struct gtq_eviction {
   int64_t w_out_strides[2];    /* element (b, h, r) at b*s[0] + h*s[1] + r      */
   int32_t* kept_dev;           /* int32 [batch][n_kv_heads][keep]: old index of */
                                /* each kept token, -1 behind the last; or NULL  */
-  int32_t* new_lens_dev;       /* int32 [batch]: min(len_b, keep)               */
+  int32_t* new_lens_dev;       /* int32 [batch]: min(len_b, keep); not the      */
+                               /* lengths that the source's layout names        */
 } gtq_eviction;
 
 /*
@@ -451,15 +459,17 @@ typedef struct gtq_eviction {
  *   dst_lay          NULL (contiguous) or a layout whose block table names the new
  *                    pages (its lengths are not read; max_blocks * 64 >= keep).
  *                    dst must not overlap the source tiles: a contiguous dst_dev
- *                    inside a contiguous src is refused, pages are the caller's
- *                    (new pages of the same pool are fine).
- *   weights_out_dev, kept_dev  must not overlap the inputs; elements of
+ *                    inside a contiguous src is refused, and so is the source's own
+ *                    block table; pages are the caller's (new pages of the same pool
+ *                    are fine).
+ *   weights_out_dev, kept_dev, new_lens_dev  must not overlap the inputs (weights_out
+ *                    at weights and new_lens on seq_lens are refused); elements of
  *                    weights_out behind the last kept token are left as they are.
  *   workspace_dev    workspace_bytes >= gtq_evict_workspace_bytes(plan, T), 256-byte
  *                    aligned, one per call that may overlap.
  * The plan's allocation stays; appends, decodes and chunks go on over the new
  * cache with new_lens_dev as its lengths.
- * Errors: INVALID, UNSUPPORTED (head_dim != 128), CUDA.
+ * Errors: INVALID, UNSUPPORTED (head_dim != 128; T above 2^31 - 1), CUDA.
  */
 GTQ_API int gtq_evict(gtq_plan* plan, const void* src_dev, int64_t T, const gtq_seq_layout* lay,
                       const gtq_eviction* ev, void* dst_dev, size_t dst_bytes,

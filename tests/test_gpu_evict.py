@@ -114,6 +114,23 @@ def test_evict(case, kind):
     assert torch.equal(before, c.packed)
 
 
+class Codes(Cache):
+    def read(self):  # nothing of it as numbers
+        pass
+
+
+@pytest.mark.parametrize("keep", [50, 70000, 262144])
+@pytest.mark.parametrize("kind", ["spread", "ties"])
+def test_evict_from_more_tokens_than_a_block_holds(keep, kind):
+    # the stretches of the blocks of a head are longer than what stays in shared memory
+    c = Codes([270000], 1, 2, 1, 1, seed=keep)
+    g = torch.Generator(device="cuda").manual_seed(keep)
+    w = torch.exp(3 * torch.randn((1, 1, c.cap), generator=g, device="cuda"))
+    if kind == "ties":
+        w = torch.where(w < 1.5, torch.zeros_like(w), torch.round(w))
+    check_evict(c, w, keep, 4, 30, *run_evict(c, w, keep, 4, 30))
+
+
 def test_evict_odd_weights():
     c = Cache([400], 2, 2, 3, 3, seed=2)
     w = torch.randn((1, 2, 400), device="cuda")

@@ -106,3 +106,31 @@ def test_evict_refuses():
     with pytest.raises(ValueError):
         gtq.gtq_evict(c.plan, c.packed, 100, w, 32, dst, lens, ws, kept=torch.zeros((2, 2, 31), dtype=torch.int32, device="cuda"))
     assert call() == gtq.GTQ_OK
+
+
+def test_outputs_that_overlap_are_refused():
+    x = Calls()
+    qs = x.q.stride()
+    for i in range(3):  # one row of out for several of q
+        s = list(x.out.stride())
+        s[i] = 0
+        assert x.attn(out_strides=(ctypes.c_int64 * 4)(*s)) == INV
+    # in place, but in another order of dims
+    assert x.attn(out=x.q.data_ptr(), out_strides=(ctypes.c_int64 * 4)(qs[0], qs[2], qs[1], 1)) == INV
+    assert x.weights(w_strides=(0, 128)) == INV and x.weights(w_strides=(256, 0)) == INV
+    c, w = x.c, torch.rand((2, 2, 128), device="cuda")
+    ws = workspace(1 << 20)
+    dst = torch.full((c.plan.packed_bytes,), 9, dtype=torch.uint8, device="cuda")
+    lens = torch.full((2,), 9, dtype=torch.int32, device="cuda")
+    before = c.seq_lens.clone(), w.clone()
+    bad = [dict(new_lens=c.seq_lens), dict(weights_out=w), dict(weights_out=torch.zeros((1, 2, 32), device="cuda").expand(2, 2, 32))]
+    for kw in bad:
+        with pytest.raises(gtq.GtqError):
+            gtq.gtq_evict(c.plan, c.packed, 100, w, 32, dst, kw.pop("new_lens", lens), ws, layout=c.layout, **kw)
+    d = Cache([100, 80], 2, 2, 3, 3, cap=128, paged=True, seed=1)
+    with pytest.raises(gtq.GtqError):  # the source's own pages
+        gtq.gtq_evict(d.plan, d.packed, 100, w, 32, d.packed, lens, ws, layout=d.layout,
+                      dst_layout=gtq.seq_layout(None, d.table))
+    torch.cuda.synchronize()
+    assert torch.equal(c.seq_lens, before[0]) and torch.equal(w, before[1])
+    assert bool((dst == 9).all()) and bool((lens == 9).all())

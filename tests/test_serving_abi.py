@@ -66,6 +66,15 @@ def test_rope_refuses_bad_calls():
     assert _call_rope(bad, _tensor()) == INV
 
 
+def test_rope_refuses_rows_that_overlap():
+    c = _rope()
+    # one row of y for several of x, and in place with another order of dims
+    assert _call_rope(c, _tensor(y=2 * P, y_strides=_strides(0, 512, 128, 1)), batch=2) == INV
+    assert _call_rope(c, _tensor(y=2 * P, y_strides=_strides(1024, 0, 128, 1))) == INV
+    assert _call_rope(c, _tensor(y=2 * P, y_strides=_strides(1024, 512, 0, 1))) == INV
+    assert _call_rope(c, _tensor(y_strides=_strides(1024, 128, 256, 1))) == INV
+
+
 def test_calls_without_a_plan():
     lib = binding.library()
     ch = binding.gtq_chunk(1, None, 1, 0, _strides(0, 128, 0, 1), _strides(0, 128, 0, 1))
