@@ -240,3 +240,87 @@ def test_two_calls_at_once_on_one_plan():
     torch.cuda.synchronize()
     for o, x in zip(outs, want):
         assert torch.equal(o, x)
+
+
+PAIRS = [
+    # lens, hkv, gq, kb, vb, paged, n, chunk_lens, causal: more than 256 rows of a KV head
+    ([65], 1, 4, 3, 3, True, 65, None, True),                         # the last row sees a tile and one token
+    ([64, 129, 1], 2, 8, 3, 2, True, 40, [40, 17, 1], True),          # sequences of one half, of less, of one token
+    ([700, 0, 333], 1, 3, 2, 2, True, 171, [171, 9, 86], True),       # 257 and 258 rows beside none
+    ([450], 1, 8, 8, 8, True, 65, None, False),
+    ([450, 190], 1, 8, 6, 5, False, 129, [129, 100], True),
+    ([8000, 130], 1, 8, 3, 3, True, 33, None, True),                  # split, and a sequence that ends in the first part
+    ([300], 1, 128, 1, 1, False, 5, None, True),
+    ([50], 1, 2, 3, 3, True, 200, None, True),                        # most rows stand before the first token
+    ([700, 0, 333], 1, 8, 2, 2, True, 120, [120, 3, 65], True),       # 960 rows, 24 of none, 520
+    ([450], 1, 8, 8, 8, True, 60, None, False),
+    ([450, 190], 2, 8, 6, 5, False, 60, [60, 33], False),
+    ([300], 1, 128, 1, 1, False, 4, None, True),
+    ([9000], 1, 4, 4, 4, True, 250, None, True),                      # split, several tiles of rows
+]
+
+
+@pytest.mark.parametrize("case", PAIRS, ids=[str(i) for i in range(len(PAIRS))])
+def test_many_rows_against_fp64(case):
+    lens, hkv, gq, kb, vb, paged, n, cl, causal = case
+    c = Cache(lens, hkv, gq, kb, vb, paged=paged, seed=len(lens) + n)
+    q = c.queries(n, seed=n)
+    for b in range(c.B):
+        if cl is not None:
+            q[b, :, cl[b]:] = float("nan")
+    out = run_chunk(c, q, n, cl, causal)
+    check_chunk(c, q, out, n, cl, causal)
+    # in place
+    ws = workspace(gtq.gtq_chunk_workspace(c.plan, c.cap, n))
+    lens_dev = None if cl is None else torch.tensor(cl, dtype=torch.int32, device="cuda")
+    gtq.gtq_chunk_attn(c.plan, c.packed, c.cap, q, q, ws, layout=c.layout, chunk_lens=lens_dev, causal=causal)
+    for b in range(c.B):
+        nb = n if cl is None else cl[b]
+        assert torch.equal(q[b, :, :nb], out[b, :, :nb])
+
+
+@pytest.mark.parametrize("n", [3, 20, 40, 90])   # each form of the kernel; 9000 tokens are split, 200 are not
+@pytest.mark.parametrize("length", [200, 9000])
+def test_nan_queries_stay_in_their_rows(n, length):
+    c = Cache([length], 1, 8, 3, 3, seed=n)
+    q = c.queries(n, seed=n)
+    want = run_chunk(c, q, n, None, True)
+    weights = run_weights(c, q, n, None, True)
+    bad = q.clone()
+    bad[0, 5, n // 2, 77] = float("nan")
+    got = run_chunk(c, bad, n, None, True)
+    assert bool(got[0, 5, n // 2].isnan().all())
+    got[0, 5, n // 2] = want[0, 5, n // 2]
+    assert torch.equal(got, want)
+    seen = length - n + n // 2 + 1
+    w = run_weights(c, bad, n, None, True)
+    assert bool(w[0, 0, :seen].isnan().all()) and bool(w[0, 0, seen:].isfinite().all())
+    assert bool((w[0, 0, seen:] == weights[0, 0, seen:]).all())
+
+
+def test_many_rows_in_a_graph_whose_lengths_change():
+    c = Cache([500, 260], 1, 8, 3, 3, paged=True, seed=17)
+    n = 40
+    q = c.queries(n, seed=3)
+    out = torch.empty_like(q)
+    cl = torch.tensor([n, n], dtype=torch.int32, device="cuda")
+    ws = workspace(gtq.gtq_chunk_workspace(c.plan, c.cap, n))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            gtq.gtq_chunk_attn(c.plan, c.packed, c.cap, q, out, ws, layout=c.layout, chunk_lens=cl, stream=s)
+    K, V = c.K, c.V
+    for lens, rows in (([500, 260], [40, 40]), ([77, 0], [1, 40]), ([129, 260], [33, 0])):
+        c.seq_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        cl.copy_(torch.tensor(rows, dtype=torch.int32))
+        out.fill_(77.0)
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            g.replay()
+        s.synchronize()
+        c.lens = lens
+        c.K = [[k[:x] for k in row] for row, x in zip(K, lens)]
+        c.V = [[v[:x] for v in row] for row, x in zip(V, lens)]
+        check_chunk(c, q, out, n, rows, True)
