@@ -289,10 +289,63 @@ __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
 
-// 32 bits from bit `at` of a word array
-__device__ __forceinline__ uint32_t bits_at(const uint32_t* x, int at) {
-  const int i = at >> 5;
-  return __funnelshift_r(x[i], x[i + 1], at & 31);
+// At least n <= 32 bits from bit `at` of a word array; the second word is read only where the bits
+// reach into it.
+__device__ __forceinline__ uint32_t bits_at(const uint32_t* x, int at, int n) {
+  const uint32_t* p = x + (at >> 5);
+  uint32_t next = 0;
+  if ((at & 31) + n > 32) next = p[1];
+  return __funnelshift_r(p[0], next, at);
+}
+
+// Where a token's codes lie in a batch of source tiles, in bits of shared memory.
+struct From {
+  int tile;   // its tile, or -1: not in this batch
+  int entry;  // its place among a row of 64: (t % 8) * 8 + t / 8, key pairs and norms
+  int value;  // its codes of dim 0
+};
+
+// The pairs of codes of 8 tokens (g + 8 u) in two slots, shifted together from the last to the first.
+// Bit j of `here`: token j of the new tile comes from this batch.
+template <int WORDS>
+__device__ __forceinline__ void gather_keys(const uint32_t* x, const From* from, uint64_t here, int g, const int (&w2)[2],
+                                            const int (&area)[2], uint32_t (&acc)[2][4]) {
+#pragma unroll
+  for (int u = 7; u >= 0; --u) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int r = WORDS - 1; r > 0; --r) acc[k][r] = __funnelshift_l(acc[k][r - 1], acc[k][r], w2[k]);
+      acc[k][0] <<= w2[k];
+    }
+    if (!((here >> (8 * u)) & 255)) continue;
+    const int tile = from[g + 8 * u].tile, entry = from[g + 8 * u].entry;
+    if (tile < 0) continue;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      acc[k][0] |= bits_at(x, tile + area[k] + w2[k] * entry, w2[k]) & ((1u << w2[k]) - 1);
+  }
+}
+
+// The codes of 16 tokens in two dims: for every (a, b) those of tokens 16 a + 8 b + 2 c + l, as
+// (dim, l) = (0, 0), (0, 1), (1, 0), (1, 1).  A token's two codes lie 2 vb bits apart in the old tile
+// as they do in the new one.
+template <int WORDS>
+__device__ __forceinline__ void gather_values(const uint32_t* x, const From* from, uint64_t here, int c, int vb, int area,
+                                              uint32_t (&acc)[8]) {
+  const uint32_t code = (1u << vb) - 1, both = code | code << (2 * vb);
+#pragma unroll
+  for (int ab = 7; ab >= 0; --ab) {
+#pragma unroll
+    for (int r = WORDS - 1; r > 0; --r) acc[r] = __funnelshift_lc(acc[r - 1], acc[r], 4 * vb);
+    acc[0] = __funnelshift_lc(0u, acc[0], 4 * vb);  // (a whole word at vb = 8)
+    if (!((here >> (8 * ab)) & 255)) continue;
+#pragma unroll
+    for (int l = 0; l < 2; ++l) {
+      const int at = from[8 * ab + 2 * c + l].value;
+      if (at >= 0) acc[0] |= (bits_at(x, at + area, 3 * vb) & both) << (l * vb);
+    }
+  }
 }
 
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ EvictArgs a, int* status) {
@@ -300,6 +353,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
   __shared__ HeadMeta m;
   __shared__ int src_tile[kTile];     // distinct source tiles, in order
   __shared__ uint16_t tok[kTile];     // token: place of its tile in that list << 8 | its index there
+  __shared__ From from[kTile];
+  __shared__ __align__(8) uint32_t in_batch[2];
   __shared__ int n_src;
   __shared__ __align__(8) uint64_t bar;
   const int head = blockIdx.y, b = head / a.hkv;
@@ -356,6 +411,17 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
             "r"(smem_addr(&bar))
             : "memory");
     }
+    if (tid < kTile) {
+      const int j = tid, v = tok[j], i = (v >> 8) - s0, js = v & 63;
+      const bool in = (unsigned)i < (unsigned)n;
+      const int at = 8 * (tb + i * (int)stage);
+      const unsigned any = __ballot_sync(0xffffffffu, in);
+      if (lane == 0) in_batch[tid >> 5] = any;
+      from[j].tile = in ? at : -1;
+      from[j].entry = (js & 7) * 8 + (js >> 3);
+      // portion (i8, g, c) holds dims 16 i8 + g and + 8 of 16 tokens
+      from[j].value = in ? at + 8192 * kb + vb * (((js & 7) >> 1) * 32 + 4 * (js >> 3) + (js & 1)) : -1;
+    }
     {  // bounded wait: after 2 s the call has failed, after 2 s more its copies are given up
       uint64_t began = 0;
       for (unsigned i = 0;; ++i) {
@@ -373,73 +439,38 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
       }
     }
     if (__syncthreads_or(!ok)) { ok = false; break; }
-    // token j: words of its old tile (null: not in this batch), and its index there
-    auto source = [&](int j, int& js) -> const uint32_t* {
-      const int v = tok[j], i = (v >> 8) - s0;
-      js = v & 63;
-      return (unsigned)i < (unsigned)n ? reinterpret_cast<const uint32_t*>(sm + tb + i * stage) : nullptr;
-    };
     // keys: portion g of slot s holds the pairs of tokens g + 8 u, 2 w bits each; a thread's two
-    // slots share the tokens.  The pairs are shifted in from the last to the first.
+    // slots share the tokens
+    const uint32_t* const words = reinterpret_cast<const uint32_t*>(sm);
+    const uint64_t here = *reinterpret_cast<const uint64_t*>(in_batch);
     {
       const int g = tid & 7;
-      int w[2], area[2];
+      int w2[2], area[2];
       uint32_t acc[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int s = (tid >> 3) + 32 * k;
-        w[k] = m.slot_width[s];
-        area[k] = 8 * m.slot_koff[s];
+        const int slot = (tid >> 3) + 32 * k;
+        w2[k] = 2 * m.slot_width[slot];
+        area[k] = 8 * m.slot_koff[slot];
       }
-#pragma unroll 2
-      for (int u = 7; u >= 0; --u) {
-        int js;
-        const uint32_t* x = source(g + 8 * u, js);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int w2 = 2 * w[k];
-          uint32_t pair = 0;
-          if (x) pair = bits_at(x, area[k] + (js & 7) * 8 * w2 + (js >> 3) * w2) & ((1u << w2) - 1);
-          acc[k][3] = __funnelshift_l(acc[k][2], acc[k][3], w2);
-          acc[k][2] = __funnelshift_l(acc[k][1], acc[k][2], w2);
-          acc[k][1] = __funnelshift_l(acc[k][0], acc[k][1], w2);
-          acc[k][0] = (acc[k][0] << w2) | pair;
-        }
-      }
+      if (__any_sync(0xffffffffu, max(w2[0], w2[1]) > 8)) gather_keys<4>(words, from, here, g, w2, area, acc);
+      else gather_keys<2>(words, from, here, g, w2, area, acc);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {  // 16 w bits at a multiple of 16 bits
-        uint16_t* o = reinterpret_cast<uint16_t*>(sm) + (area[k] >> 4) + g * w[k];
+        const int w = w2[k] >> 1;
+        uint16_t* o = reinterpret_cast<uint16_t*>(sm) + (area[k] >> 4) + g * w;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (i < w[k]) o[i] |= (uint16_t)(acc[k][i >> 1] >> (16 * (i & 1)));
+          if (i < w) o[i] |= (uint16_t)(acc[k][i >> 1] >> (16 * (i & 1)));
       }
     }
-    // values: portion (i8, g, c) holds dims 16 i8 + g and + 8 of the tokens 16 a + 8 b + 2 c + l: for
-    // every (a, b) the codes of (dim, l) = (0, 0), (0, 1), (1, 0), (1, 1).  A token's two codes lie
-    // 2 vb bits apart in the old tile as they do in the new one.
     if (vb) {
-      static_assert(kMoveThreads == 256, "one portion a thread");
-      const uint32_t code = (1u << vb) - 1, both = code | code << (2 * vb);
-      const int c = tid & 3, area = 8192 * kb + (tid >> 2) * 128 * vb;
+      static_assert(kMoveThreads == 256, "one portion of values a thread");
+      const int area = (tid >> 2) * 128 * vb;
       uint32_t acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 2
-      for (int ab = 7; ab >= 0; --ab) {
-        uint32_t four = 0;
-#pragma unroll
-        for (int l = 0; l < 2; ++l) {
-          int js;
-          const uint32_t* x = source(8 * ab + 2 * c + l, js);
-          if (x) {
-            const int xs = 4 * (js >> 3) + (js & 1);
-            four |= (bits_at(x, area + ((js & 7) >> 1) * 32 * vb + xs * vb) & both) << (l * vb);
-          }
-        }
-        // shift the portion by 4 vb bits (a whole word at vb = 8)
-#pragma unroll
-        for (int r = 7; r > 0; --r)
-          if (r < vb) acc[r] = __funnelshift_lc(acc[r - 1], acc[r], 4 * vb);
-        acc[0] = __funnelshift_lc(0u, acc[0], 4 * vb) | four;
-      }
+      if (vb <= 2) gather_values<2>(words, from, here, tid & 3, vb, area, acc);
+      else if (vb <= 4) gather_values<4>(words, from, here, tid & 3, vb, area, acc);
+      else gather_values<8>(words, from, here, tid & 3, vb, area, acc);
       uint32_t* o = out + 256 * kb + tid * vb;
 #pragma unroll
       for (int r = 0; r < 8; ++r)
@@ -449,12 +480,10 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
     const int n_rows = (vb ? 1 : 0) + m.n_groups;
     for (int i = tid; i < n_rows * kTile; i += kMoveThreads) {
       const int row = i >> 6, at = i & 63, j = (at & 7) * 8 + (at >> 3);  // entry `at` is of token j
-      int js;
-      const uint32_t* x = source(j, js);
-      if (!x) continue;
+      const int tile = from[j].tile;
+      if (tile < 0) continue;
       const int o = 512 * (kb + vb) + row * 64;
-      reinterpret_cast<uint16_t*>(sm)[o + at] =
-          reinterpret_cast<const uint16_t*>(x)[o + (js & 7) * 8 + (js >> 3)];
+      reinterpret_cast<uint16_t*>(sm)[o + at] = reinterpret_cast<const uint16_t*>(sm)[(tile >> 4) + o + from[j].entry];
     }
     __syncthreads();  // the batch is read before the next one lands on it
   }
@@ -495,7 +524,7 @@ cudaError_t launch_evict(const gtq_plan* p, const uint8_t* src, int64_t T, const
   a.kb = p->cfg.k_bits;
   a.vb = p->cfg.v_bits;
   int blocks = 1;
-  while (blocks < kSelCluster && T > (int64_t)blocks * kSelTokens) blocks *= 2;
+  while (blocks < kSelCluster && T > (int64_t)blocks * kSelTokens && 2 * blocks * p->n_heads <= p->n_sms) blocks *= 2;
   const int64_t stretch = (T + blocks - 1) / blocks + kPer;
   a.held = (int)std::min<int64_t>(stretch, kHeld);
   const size_t sel_smem = (size_t)(a.held + a.held / 16 + 1) * sizeof(uint32_t) +
