@@ -10,12 +10,13 @@
 //
 // An element is cb[code] / 16 * norm: the power of two keeps the largest norm
 // (65504) times the largest centroid in the fp16 range, and is undone in the
-// queries and at the end.
+// queries and at the end.  Where an element is split into hi + lo, the codebook's low parts stay
+// as they are and take norm / 16 instead: a 16th of most of them would be an fp16 subnormal.
 //
 // Keys of widths up to 4 take a pair of codes in one lookup, every lane by its own
 // width (mask, table, multiplier), so that four slots of different widths run as
 // one instruction stream (code per width, one after another for the widths of a
-// warp, measured 1.3 times slower).  Wider codes, and slots that leave a low part, are
+// warp, made a chunk of 512 rows 1.09 times slower).  Wider codes, and slots that leave a low part, are
 // looked up one by one.  All lookups of a portion come before its stores: a load may
 // not pass a store whose address the compiler cannot tell apart.
 #pragma once
@@ -28,7 +29,7 @@ namespace gtq {
 // Lookup tables in shared memory (fp16 values of the codebook / 16): pair tables of
 // widths 3, 2, 1 with a copy per lane, as they lie in the decode image (kTabP32W3
 // .. kTabS32W5), a pair table of width 4 in one copy, single codes of all widths
-// (kTabSS: hi | lo << 16), and a zero.
+// (kTabSS: hi | lo << 16, the low parts not divided), and a zero.
 constexpr uint32_t kDqPairs = 0;
 constexpr uint32_t kDqPairBytes = kTabS32W5 - kTabP32W3;
 constexpr uint32_t kDqPair4 = kDqPairs + kDqPairBytes;
@@ -49,7 +50,8 @@ __device__ __forceinline__ void load_dequant_tables(uint8_t* tab, const uint4* i
   auto scaled = [](uint32_t v) { return as_u32(__hmul2(as_h2(v), __float2half2_rn(0.0625f))); };
   for (int i = tid; i < (int)(kDqPairBytes / 4); i += n_threads)
     reinterpret_cast<uint32_t*>(tab + kDqPairs)[i] = scaled(pp[i]);
-  for (int i = tid; i < 512; i += n_threads) reinterpret_cast<uint32_t*>(tab + kDqSingles)[i] = scaled(ss[i]);
+  for (int i = tid; i < 512; i += n_threads)
+    reinterpret_cast<uint32_t*>(tab + kDqSingles)[i] = as_u32(__hmul2(as_h2(ss[i]), __floats2half2_rn(0.0625f, 1.f)));
   for (int i = tid; i < 256; i += n_threads)
     reinterpret_cast<uint32_t*>(tab + kDqPair4)[i] =
         scaled(__byte_perm(ss[kSingleOff(4) / 4 + (i & 15)], ss[kSingleOff(4) / 4 + (i >> 4)], 0x5410));
@@ -61,7 +63,7 @@ __device__ __forceinline__ void load_dequant_tables_lo(uint8_t* tab, const uint4
   const uint32_t* ss = reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(image) + kTabSS);
   auto pair = [&](int w, int i) {
     const uint32_t* e = ss + kSingleOff(w) / 4;
-    return as_u32(__hmul2(as_h2(__byte_perm(e[i & ((1 << w) - 1)], e[i >> w], 0x7632)), __float2half2_rn(0.0625f)));
+    return __byte_perm(e[i & ((1 << w) - 1)], e[i >> w], 0x7632);
   };
 #pragma unroll
   for (int w = 1; w <= 3; ++w)
@@ -201,6 +203,7 @@ __device__ __forceinline__ void keys_by_pair_split(const KeyLane& k, const KeyRa
   x[0] = __funnelshift_r(r.x[0], r.x[1], odd);
   x[1] = __funnelshift_rc(x[0], r.x[1] >> odd, 4 * w2);
   const uint32_t nw[4] = {r.n.x, r.n.y, r.n.z, r.n.w};
+  const __half2 sixteenth = __float2half2_rn(0.0625f);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     uint32_t v[4], l[4];
@@ -217,7 +220,8 @@ __device__ __forceinline__ void keys_by_pair_split(const KeyLane& k, const KeyRa
       const __half2 n = as_h2(nw[2 * i + (u >> 1)]), nn = (u & 1) ? __high2half2(n) : __low2half2(n);
       const __half2 p = __hmul2(as_h2(v[u]), nn);
       sts32(d + 1024 * u, as_u32(p));
-      sts32(d + 1024 * u + lo_dst, as_u32(__hfma2(as_h2(l[u]), nn, __hfma2(as_h2(v[u]), nn, __hneg2(p)))));
+      sts32(d + 1024 * u + lo_dst,
+            as_u32(__hfma2(as_h2(l[u]), __hmul2(nn, sixteenth), __hfma2(as_h2(v[u]), nn, __hneg2(p)))));
     }
   }
 }
@@ -261,7 +265,8 @@ __device__ __forceinline__ void keys_by_code(const KeyLane& k, const KeyRaw& r, 
       sts32(d + 4096 * half + 1024 * u, as_u32(p));
       // hi * n - fp16(hi * n) is exact in one fma (above the subnormals); lo * n joins it
       if (low)
-        sts32(dl + (4 * half + u) * lo_rows, as_u32(__hfma2(lo, nn, __hfma2(hi, nn, __hneg2(p)))));
+        sts32(dl + (4 * half + u) * lo_rows,
+              as_u32(__hfma2(lo, __hmul2(nn, __float2half2_rn(0.0625f)), __hfma2(hi, nn, __hneg2(p)))));
     }
   }
 }
