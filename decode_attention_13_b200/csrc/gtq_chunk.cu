@@ -3,10 +3,10 @@
 // in their rotated bases as the cache codes them.
 //
 // A block takes up to 256 rows of one KV head (row r = query head r % Gq of new
-// token r / Gq: rows of one token share their limit) and a stretch of its tokens,
-// 128 at a time.  Both products run as tcgen05.mma with fp32 accumulators in
-// tensor memory; the codes are turned into fp16 operands once per block in shared
-// memory and serve all its rows.
+// token r / Gq: rows of one token share their limit), or a pair of CTAs up to 512,
+// and a stretch of its tokens, 128 at a time.  Both products run as tcgen05.mma with
+// fp32 accumulators in tensor memory; the codes are turned into fp16 operands once per
+// block in shared memory and serve all its rows.
 //   * warps 0-3, 4-7   softmax: thread = row (tensor-memory lane).  Scores are read
 //     from tensor memory, P goes back over them as fp16 and is the A operand of the
 //     second product.  The reference maximum moves only when it grew by more than
@@ -16,19 +16,33 @@
 //     group has written its P: one hand-off less than a warp of its own.
 //   * warps 8-15       tiles of codes to operands (gtq_dequant.cuh): keys run a step ahead
 //     of values, and a warp's loads of the one are in flight while it works on the other.
-//     (24 warps, 16 of them here, measured 1.4 times slower: at 80 registers the loops spill.)
+//     (24 warps, 16 of them here, measured 1.06 times slower over 512 rows: 80 registers a
+//     thread are too few for it.)
 // With 129 rows or more (NQ = 2) the two softmax groups take 128 rows each: while
-// one group's products run, the other computes.  With fewer (NQ = 1) they share
-// the rows and take the token blocks in turns, each with an output of its own;
-// the last product joins them.
-// Scores: q (hi) k (hi) over all 128 coordinates, plus q (lo) k (hi) and q (hi) k (lo) over
-// the first 16, the widest codes: fp16 roundings then stay on coordinates whose part of a
-// logit is small.  q is scaled by log2(e), so probabilities are powers of 2.
-// The queries' rotation and the values' way back are products of the same block, with the
-// rotations split into fp16 hi + lo and (for the way back) the output too.
+// one group's products run, the other computes, and they take turns with the exponentials.
+// With fewer (NQ = 1) they share the rows and take the token blocks in turns, each with an
+// output of its own; the last product joins them.
+// In a pair (cta_group::2) each CTA has 256 rows and turns half of every step's codes: 64 of
+// its 128 tokens' keys, 64 of the 128 dims of its values.  The even CTA issues both CTAs'
+// products.
 // With few blocks' worth of rows, the tokens are split over blocks in stretches of equal
 // length; each leaves a normalised output with its maximum and sum, and merge_kernel joins
 // them.
+//
+// Roundings.  fp16, half a step 2^-11: the turned keys, P, the values, the result.  Scores:
+// q (hi) k (hi) over all 128 coordinates, plus q (lo) k (hi) and q (hi) k (lo) over
+// the first 16, the widest codes, which carry most of a logit: the error that is left in a
+// logit comes from coordinates whose part of it is small.  P's sum is taken before P is
+// rounded.  q is scaled by log2(e), so probabilities are powers of 2.  The queries' rotation
+// and the values' way back are products of the same block, with the rotations split into
+// fp16 hi + lo and (for the way back) the output too.  All sums are fp32.  A row comes out
+// within 4e-4 of attention in 64 bits (2-norm), 2e-4 of it the result's own rounding.
+//
+// What bounds it: up to 128 rows, turning codes (about 4000 cycles a step of 128 tokens; 40
+// rows over 2 x 131072 tokens, 3 bits: 60 us for 29 MB).  With pairs, the chain from a step's
+// scores over the softmax and P to its products, about 5200 cycles a step against 2300 of
+// tcgen05.mma: 8192 rows over 2 x 131072 tokens, 3 bits, take 1.44 ms (0.76 PFLOP/s), 4000
+// rows over 8 x 32768, 2 bits, 0.74 ms (0.72 PFLOP/s).
 #include <algorithm>
 
 #include "gtq_attn.cuh"
@@ -863,7 +877,8 @@ size_t chunk_workspace(const gtq_plan* p, int64_t T, int64_t n) {
 cudaError_t launch_chunk(const gtq_plan* p, const uint8_t* packed, int64_t T, const SeqMap& sm,
                          const gtq_chunk& ch, const __half* q, __half* out, uint8_t* workspace,
                          cudaStream_t s) {
-  // (16 sequences x 4 KV heads of 7 queries, up to 16384 tokens each: 213 us as a chunk of one row)
+  // One token: 16 sequences x 4 KV heads of 7 queries, up to 16384 tokens each, take 91 us this way
+  // and 213 us as a chunk, whose products are then mostly of rows that are not there.
   if (ch.n_tokens == 1) return launch_token(p, packed, T, sm, ch, q, out, workspace, s);
   const Cut c = cut_of(p, T, ch.n_tokens);
   ChunkArgs a = {};
@@ -913,6 +928,8 @@ cudaError_t launch_chunk(const gtq_plan* p, const uint8_t* packed, int64_t T, co
   e = cudaLaunchKernelEx(&cfg, kernel, a);
   if (e != cudaSuccess || c.splits == 1) return e;
   const int64_t rows = ch.n_tokens * p->g_q;
+  // eight warps a row from eight parts on (64 rows in about 70 parts: 61 us for the call, 80 with one
+  // warp a row); with fewer, one (8 heads of 1024 rows in a few parts: 232 us, 241 with eight)
   if (c.splits >= 8)
     return launch_overlapped(merge_kernel<8>, dim3((unsigned)rows, (unsigned)p->n_heads), 256, 0, s, a);
   return launch_overlapped(merge_kernel<1>, dim3((unsigned)((rows + 7) / 8), (unsigned)p->n_heads), 256, 0, s, a);
