@@ -324,3 +324,49 @@ def test_many_rows_in_a_graph_whose_lengths_change():
         c.K = [[k[:x] for k in row] for row, x in zip(K, lens)]
         c.V = [[v[:x] for v in row] for row, x in zip(V, lens)]
         check_chunk(c, q, out, n, rows, True)
+
+
+def test_one_token_of_empty_and_absent_sequences():
+    c = Cache([0, 200, 64], 2, 4, 3, 3, paged=True, seed=61)
+    q = c.queries(1, seed=62)
+    for cl in (None, [1, 0, 1]):
+        check_chunk(c, q, run_chunk(c, q, 1, cl, True), 1, cl, True)
+
+
+def test_far_pages():
+    # the same pages beyond 4 GiB of a pool
+    c = Cache([300, 130], 2, 4, 3, 3, paged=True, seed=71)
+    page = c.hkv * c.tb
+    shift = (5 << 30) // page
+    pool = torch.empty((shift + c.pages) * page, dtype=torch.uint8, device="cuda")
+    pool[shift * page:] = c.packed
+    far_table = c.table + shift     # (a layout holds addresses, not tensors)
+    far = gtq.seq_layout(c.seq_lens, far_table)
+    for n in (1, 7, 40, 80):    # 4 to 320 rows
+        q = c.queries(n, seed=n)
+        want, w_want = run_chunk(c, q, n, None, True), run_weights(c, q, n, None, True)
+        near = c.packed, c.layout
+        c.packed, c.layout = pool, far
+        try:
+            got, w_got = run_chunk(c, q, n, None, True), run_weights(c, q, n, None, True)
+        finally:
+            c.packed, c.layout = near
+        assert torch.equal(got, want) and torch.equal(w_got, w_want)
+
+
+def test_far_heads():
+    # a capacity whose second head lies beyond 4 GiB
+    c = Cache([300], 2, 4, 3, 3, seed=73)
+    cap = (5 << 30) // c.tb * 64
+    plan = gtq.gtq_alloc_bits_ex(gtq.make_config(1, c.hq, 2, 3, 3, cap), c.k, 300, c.layout)
+    packed = torch.empty(plan.packed_bytes, dtype=torch.uint8, device="cuda")
+    gtq.gtq_quantize_pack_ex(plan, c.k, c.v, 0, 300, packed, c.layout)
+    for n in (1, 7, 80):
+        q = c.queries(n, seed=n)
+        want, w_want = run_chunk(c, q, n, None, True, T=300), run_weights(c, q, n, None, True)
+        out, w = torch.empty_like(q), torch.full_like(w_want, 77.0)
+        gtq.gtq_chunk_attn(plan, packed, 300, q, out, workspace(gtq.gtq_chunk_workspace(plan, 300, n)), layout=c.layout)
+        gtq.gtq_attn_weights(plan, packed, 300, q, w, workspace(gtq.gtq_weights_workspace(plan, 300, n)), layout=c.layout)
+        torch.cuda.synchronize()
+        assert gtq.gtq_status(plan) == gtq.GTQ_OK
+        assert torch.equal(out, want) and torch.equal(w[:, :, :300], w_want[:, :, :300])

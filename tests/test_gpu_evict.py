@@ -152,6 +152,39 @@ def test_evict_without_the_optional_outputs_and_with_strides():
     check_evict(c, w.contiguous(), 150, 4, 8, *a)
 
 
+def test_evict_with_a_bound_below_the_lengths():
+    # T bounds every sequence: as if each held at most T tokens
+    c = Cache([500, 90], 2, 2, 3, 3, paged=True, seed=14)
+    w = torch.rand((2, 2, 500), device="cuda")
+    got = run_evict(c, w, 120, 4, 16, T=200, dst_paged=True)
+    c.lens = [200, 90]
+    check_evict(c, w, 120, 4, 16, *got)
+
+
+def test_evict_far_pages():
+    # from pages beyond 4 GiB of a pool to others there
+    c = Cache([700, 333], 2, 2, 3, 3, paged=True, seed=15)
+    w = torch.rand((2, 2, 700), device="cuda")
+    page = c.hkv * c.tb
+    shift, n = (5 << 30) // page, (200 + 63) // 64
+    far = c.table + shift
+    pool = torch.full(((shift + c.pages + 2 * n) * page,), 0x5A, dtype=torch.uint8, device="cuda")
+    pool[shift * page:(shift + c.pages) * page] = c.packed
+    new = shift + c.pages + torch.arange(2 * n, dtype=torch.int32, device="cuda").reshape(2, n)
+    lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+    kept = torch.zeros((2, 2, 200), dtype=torch.int32, device="cuda")
+    wo = torch.full((2, 2, 200), 77.0, device="cuda")
+    gtq.gtq_evict(c.plan, pool, 700, w, 200, pool, lens, workspace(gtq.gtq_evict_workspace(c.plan, 700)), n_first=4,
+                  n_recent=20, layout=gtq.seq_layout(c.seq_lens, far), dst_layout=gtq.seq_layout(None, new),
+                  weights_out=wo, kept=kept)
+    torch.cuda.synchronize()
+    assert gtq.gtq_status(c.plan) == gtq.GTQ_OK
+    assert torch.equal(pool[shift * page:(shift + c.pages) * page], c.packed)
+    assert bool((pool[:shift * page] == 0x5A).all())
+    dst = pool[(shift + c.pages) * page:].clone()
+    check_evict(c, w, 200, 4, 20, dst, new - (shift + c.pages), lens, kept, wo)
+
+
 def test_evict_in_a_graph_with_growing_lengths():
     # one captured call, replayed after the lengths changed: they are read on the device
     c = Cache([600, 500], 1, 4, 3, 3, seed=8)
