@@ -2,17 +2,18 @@
 // and last tokens and those with the largest weights stay, and their codes move
 // to another packed cache.  Two launches.
 //
-// select_kernel: one cluster of up to 8 blocks per head.  Each block holds its stretch
+// select_kernel: one cluster of up to 16 blocks per head.  Each block holds its stretch
 // of tokens in shared memory as order-preserving integers of their weights (HBM is
 // read once; tokens beyond that memory are read again from L2).  The weight that the
 // last chosen token has is found digit by digit (11, 11 and 10 bits): each block
-// counts the digits of its stretch, the cluster adds the counts through distributed
-// shared memory, and every block finds the digit where the count from the top passes
-// what is still wanted.  Then each thread counts 16 neighbouring tokens, one prefix sum
+// counts the digits of its stretch and adds up its share of the digits over the cluster
+// (distributed shared memory), and every block finds the digit where the count from the
+// top passes what is still wanted, in the one share that holds it (2 heads of 131072
+// tokens: 47 us for the call, 51 where every block read all counts).  Then each thread counts 16 neighbouring tokens, one prefix sum
 // gives it its place, and it writes the indices of those that stay: tokens above that
 // weight, and as many with exactly that weight, lowest index first, as are missing.
 // Bound by the latencies of its dozen block- and cluster-wide steps: 26 us for 64 heads of
-// 16384 tokens (4 MB of weights), 35 us for 2 heads of 131072.
+// 16384 tokens (4 MB of weights), 31 us for 2 heads of 131072.
 //
 // move_kernel: one block per new tile and head.  The tiles that its 64 tokens
 // come from arrive by bulk copy, a batch at a time; a thread owns portions of the
@@ -35,7 +36,8 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelBins = 2048;
-constexpr int kSelCluster = 8;       // blocks per head at most (portable cluster size)
+constexpr int kSelCluster = 16;      // blocks per head at most (2 heads of 524288 tokens: 114 us for the
+                                     // call, 170 with 8; of 131072: 47 with either)
 constexpr int kSelTokens = 4096;     // tokens that are worth a block of their own
 constexpr int kPer = 16;             // neighbouring tokens of a thread
 constexpr int kHeld = 32768;         // tokens of a block that stay in shared memory
@@ -103,6 +105,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
   extern __shared__ uint32_t keys[];  // token i of the stretch at i + i / 16: a thread's 16 neighbours
                                       // then lie in as many banks as its warp's need
   __shared__ __align__(16) int hist[kSelBins];
+  __shared__ __align__(16) int slice[2][kSelBins];  // this block's share of the digits, counted over all blocks
+  __shared__ int slice_sum[2];
   __shared__ int warp_sums[32];
   __shared__ int found[2];   // digit, and the count above it
   __shared__ int counts[2];  // this block's tokens that are sure to stay, and those at the weight
@@ -129,7 +133,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
   auto key_at = [&](int i) { return i < held ? keys[i + (i >> 4)] : order_key(w[i]); };
   uint32_t prefix = 0;
   if (!all) {
-    for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
+    for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = slice[0][i] = 0;
+    if (tid == 0) slice_sum[0] = 0;
 #pragma unroll 4
     for (int i = tid; i < held; i += kSelThreads) keys[i + (i >> 4)] = order_key(w[i]);
     __syncthreads();
@@ -161,43 +166,64 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
       zeros = __reduce_add_sync(0xffffffffu, zeros);
       if (lane == 0 && zeros) atomicAdd(&hist[zero_bin], zeros);
       cluster.sync();
-      // digits from the top, four a thread (16 bytes of every block's counts)
-      const int n_bins = 1 << bits, d0 = n_bins - 4 - 4 * tid;
+      // every block adds up its share of the digits, ...
+      const int n_bins = 1 << bits, share = n_bins / blocks, quads = share / 4;
+      int* const sums = slice[pass & 1];
+      int sum = 0;
+      static_assert(kSelBins / 4 <= kSelThreads, "one quad of digits a thread");
+      if (tid < n_bins / 4) {
+        const int r = tid / quads, at = 4 * (tid - r * quads);
+        const int4 v = *reinterpret_cast<const int4*>(cluster.map_shared_rank(hist, r) + rank * share + at);
+        if (v.x) atomicAdd(&sums[at], v.x);
+        if (v.y) atomicAdd(&sums[at + 1], v.y);
+        if (v.z) atomicAdd(&sums[at + 2], v.z);
+        if (v.w) atomicAdd(&sums[at + 3], v.w);
+        sum = v.x + v.y + v.z + v.w;
+      }
+      sum = __reduce_add_sync(0xffffffffu, sum);
+      if (lane == 0 && sum) atomicAdd(&slice_sum[pass & 1], sum);
+      cluster.sync();
+      // ... and reads the share in which the count from the top (lane 0) passes `want`
+      int in_share = lane < blocks ? *cluster.map_shared_rank(&slice_sum[pass & 1], blocks - 1 - lane) : 0;
+      int upto = in_share;
+#pragma unroll
+      for (int o = 1; o < kSelCluster; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      const unsigned passes = __ballot_sync(0xffffffffu, upto - in_share < want && upto >= want);
+      const int top = passes ? __ffs(passes) - 1 : 0, f = blocks - 1 - top;
+      const int above_share = __shfl_sync(0xffffffffu, upto - in_share, top);
+      const int d0 = share - 4 - 4 * tid;
       int c[4] = {0, 0, 0, 0};
       if (d0 >= 0) {
-        int4 v[kSelCluster];
-#pragma unroll
-        for (int r = 0; r < kSelCluster; ++r)
-          if (r < blocks) v[r] = *reinterpret_cast<const int4*>(cluster.map_shared_rank(hist, r) + d0);
-#pragma unroll
-        for (int r = 0; r < kSelCluster; ++r)
-          if (r < blocks) {
-            c[0] += v[r].w;
-            c[1] += v[r].z;
-            c[2] += v[r].y;
-            c[3] += v[r].x;
-          }
+        const int4 v = *reinterpret_cast<const int4*>(cluster.map_shared_rank(sums, f) + d0);
+        c[0] = v.w;
+        c[1] = v.z;
+        c[2] = v.y;
+        c[3] = v.x;
       }
       int total;
-      int over = block_scan(c[0] + c[1] + c[2] + c[3], warp_sums, total);
+      int over = above_share + block_scan(c[0] + c[1] + c[2] + c[3], warp_sums, total);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (over < want && over + c[e] >= want) {
-          found[0] = d0 + 3 - e;
+          found[0] = f * share + d0 + 3 - e;
           found[1] = over;
         }
         over += c[e];
       }
-      // no block clears its counts while another still reads them
-      cluster.sync();
+      // (counts are read by others before the exchange's second barrier, shares after it: the other
+      // share's last readers have passed the next digit's first barrier)
+      for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = slice[(pass + 1) & 1][i] = 0;
+      if (tid == 0) slice_sum[(pass + 1) & 1] = 0;
+      __syncthreads();
       if (want > 0) {
         prefix |= (uint32_t)found[0] << shift;
         want -= found[1];
       } else {  // only the first and last tokens stay: nothing is above the largest integer
         prefix = ~0u;
       }
-      for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
     }
   }
   // want: how many of the tokens whose integer is `prefix` stay
@@ -534,6 +560,8 @@ cudaError_t launch_evict(const gtq_plan* p, const uint8_t* src, int64_t T, const
   const size_t sel_smem = (size_t)(a.held + a.held / 16 + 1) * sizeof(uint32_t) +
                           std::min<int64_t>(stretch, kSelThreads * kPer) * sizeof(uint16_t);
   cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sel_smem);
+  if (e == cudaSuccess)  // clusters above 8 blocks
+    e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.dynamicSmemBytes = sel_smem;

@@ -131,6 +131,13 @@ def test_evict_from_more_tokens_than_a_block_holds(keep, kind):
     check_evict(c, w, keep, 4, 30, *run_evict(c, w, keep, 4, 30))
 
 
+def test_evict_from_half_a_million_tokens():
+    c = Codes([530000], 1, 1, 1, 1, seed=3)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    w = torch.round(torch.exp(3 * torch.randn((1, 1, c.cap), generator=g, device="cuda")) * 8)
+    check_evict(c, w, 30000, 4, 30, *run_evict(c, w, 30000, 4, 30))
+
+
 def test_evict_odd_weights():
     c = Cache([400], 2, 2, 3, 3, seed=2)
     w = torch.randn((1, 2, 400), device="cuda")
