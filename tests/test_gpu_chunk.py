@@ -333,6 +333,17 @@ def test_one_token_of_empty_and_absent_sequences():
         check_chunk(c, q, run_chunk(c, q, 1, cl, True), 1, cl, True)
 
 
+def same(a, b, n, c):
+    """The same bits; for one token, whose decode kernel adds its parts up as its blocks end, two fp32 results differ by
+    the roundings of sums in another order: of T weights times values (weights sum to 1: each rounding is at most 2^-24
+    of the largest value) and of 128 in the rotation, twice; and the fp16 ones by those and half a step, twice."""
+    if n > 1:
+        return torch.equal(a, b)
+    a, b = a.double(), b.double()
+    largest = max(np.abs(v).max() for row in c.V for v in row if v.size)
+    return bool(((a - b).abs() <= 2 * 2.0 ** -11 * b.abs() + 2 * (max(c.lens) + 128) * 2.0 ** -24 * largest).all())
+
+
 def test_far_pages():
     # the same pages beyond 4 GiB of a pool
     c = Cache([300, 130], 2, 4, 3, 3, paged=True, seed=71)
@@ -351,7 +362,7 @@ def test_far_pages():
             got, w_got = run_chunk(c, q, n, None, True), run_weights(c, q, n, None, True)
         finally:
             c.packed, c.layout = near
-        assert torch.equal(got, want) and torch.equal(w_got, w_want)
+        assert same(got, want, n, c) and torch.equal(w_got, w_want)
 
 
 def test_far_heads():
@@ -369,4 +380,4 @@ def test_far_heads():
         gtq.gtq_attn_weights(plan, packed, 300, q, w, workspace(gtq.gtq_weights_workspace(plan, 300, n)), layout=c.layout)
         torch.cuda.synchronize()
         assert gtq.gtq_status(plan) == gtq.GTQ_OK
-        assert torch.equal(out, want) and torch.equal(w[:, :, :300], w_want[:, :, :300])
+        assert same(out, want, n, c) and torch.equal(w[:, :, :300], w_want[:, :, :300])
