@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
     const uint32_t tab = sb + M::tab;
     for (int i = dtid; i < (int)(sizeof(HeadMeta) / 4); i += 32 * kDqWarps)
       reinterpret_cast<uint32_t*>(&ms.m)[i] = reinterpret_cast<const uint32_t*>(a.meta + head)[i];
-    load_dequant_tables(sm + M::tab, a.dec_image, dtid, 32 * kDqWarps);
+    load_dequant_tables<false>(sm + M::tab, a.dec_image, dtid, 32 * kDqWarps);
     asm volatile("bar.sync 4, %0;" ::"n"(32 * kDqWarps) : "memory");
     // Keys: quads dw and 15 - dw of both tiles of a step, or (pairs) of this CTA's one, whose tokens
     // are its half of the operand's rows.  Values: 16 dims of both tiles, or (pairs) of one of them,
@@ -599,14 +599,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
         // rows behind the last tile: whatever they hold, their scores do not count
         if (key_tile(j, i) >= nt) continue;
         const uint32_t row = dst + i * 8192;
-        if (code0) keys_by_code(k0, r0[i], tab, row, low, dst + M::klo + i * 2048 + lo_lane, 256);
+        if (code0) keys_by_code<false>(k0, r0[i], tab, row, low, dst + M::klo + i * 2048 + lo_lane, 256);
         else keys_by_pair(k0, r0[i], row);
         if (!code1) {
           keys_by_pair(k1, r1[i], row);
         } else {  // widths above 4 beyond the first half of the slots: fetched when they are due
           KeyRaw r;
           load_keys<5>(r, kp[i], k1);
-          keys_by_code(k1, r, tab, row, false, 0, 0);
+          keys_by_code<false>(k1, r, tab, row, false, 0, 0);
         }
       }
     };

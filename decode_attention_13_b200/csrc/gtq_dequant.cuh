@@ -10,8 +10,10 @@
 //
 // An element is cb[code] / 16 * norm: the power of two keeps the largest norm
 // (65504) times the largest centroid in the fp16 range, and is undone in the
-// queries and at the end.  Where an element is split into hi + lo, the codebook's low parts stay
-// as they are and take norm / 16 instead: a 16th of most of them would be an fp16 subnormal.
+// queries and at the end.  Where low parts have to hold to their last bits (FINE), the
+// codebook's stay as they are and take norm / 16 instead: a 16th of most of them is an fp16
+// subnormal.  (Not where other roundings to fp16 stand beside them: it costs a chunk 1.5% of its
+// time.)
 //
 // Keys of widths up to 4 take a pair of codes in one lookup, every lane by its own
 // width (mask, table, multiplier), so that four slots of different widths run as
@@ -29,7 +31,7 @@ namespace gtq {
 // Lookup tables in shared memory (fp16 values of the codebook / 16): pair tables of
 // widths 3, 2, 1 with a copy per lane, as they lie in the decode image (kTabP32W3
 // .. kTabS32W5), a pair table of width 4 in one copy, single codes of all widths
-// (kTabSS: hi | lo << 16, the low parts not divided), and a zero.
+// (kTabSS: hi | lo << 16; FINE: the low parts not divided), and a zero.
 constexpr uint32_t kDqPairs = 0;
 constexpr uint32_t kDqPairBytes = kTabS32W5 - kTabP32W3;
 constexpr uint32_t kDqPair4 = kDqPairs + kDqPairBytes;
@@ -42,6 +44,7 @@ __device__ __forceinline__ __half2 as_h2(uint32_t v) { return *reinterpret_cast<
 __device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
 
 // Copies the tables from the decode image (all threads of the block).
+template <bool FINE>
 __device__ __forceinline__ void load_dequant_tables(uint8_t* tab, const uint4* image, int tid,
                                                     int n_threads) {
   const uint8_t* img = reinterpret_cast<const uint8_t*>(image);
@@ -51,7 +54,7 @@ __device__ __forceinline__ void load_dequant_tables(uint8_t* tab, const uint4* i
   for (int i = tid; i < (int)(kDqPairBytes / 4); i += n_threads)
     reinterpret_cast<uint32_t*>(tab + kDqPairs)[i] = scaled(pp[i]);
   for (int i = tid; i < 512; i += n_threads)
-    reinterpret_cast<uint32_t*>(tab + kDqSingles)[i] = as_u32(__hmul2(as_h2(ss[i]), __floats2half2_rn(0.0625f, 1.f)));
+    reinterpret_cast<uint32_t*>(tab + kDqSingles)[i] = as_u32(__hmul2(as_h2(ss[i]), __floats2half2_rn(0.0625f, FINE ? 1.f : 0.0625f)));
   for (int i = tid; i < 256; i += n_threads)
     reinterpret_cast<uint32_t*>(tab + kDqPair4)[i] =
         scaled(__byte_perm(ss[kSingleOff(4) / 4 + (i & 15)], ss[kSingleOff(4) / 4 + (i >> 4)], 0x5410));
@@ -228,6 +231,7 @@ __device__ __forceinline__ void keys_by_pair_split(const KeyLane& k, const KeyRa
 
 // Any width, code by code.  With `low`, the rests of the products beyond fp16 go to dl, the lane's
 // place among core matrices of 8 rows x 16 bytes (lo_rows bytes from one 8 tokens to the next).
+template <bool FINE>
 __device__ __forceinline__ void keys_by_code(const KeyLane& k, const KeyRaw& r, uint32_t tab,
                                              uint32_t dst, bool low, uint32_t dl, uint32_t lo_rows) {
   const uint32_t w = k.w, mask = (1u << w) - 1, odd = (k.src & 2u) * 8u;
@@ -266,7 +270,7 @@ __device__ __forceinline__ void keys_by_code(const KeyLane& k, const KeyRaw& r, 
       // hi * n - fp16(hi * n) is exact in one fma (above the subnormals); lo * n joins it
       if (low)
         sts32(dl + (4 * half + u) * lo_rows,
-              as_u32(__hfma2(lo, __hmul2(nn, __float2half2_rn(0.0625f)), __hfma2(hi, nn, __hneg2(p)))));
+              as_u32(__hfma2(lo, FINE ? __hmul2(nn, __float2half2_rn(0.0625f)) : nn, __hfma2(hi, nn, __hneg2(p)))));
     }
   }
 }

@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
     const int dw = warp - kReadWarps, dtid = tid - 32 * kReadWarps;
     for (int i = dtid; i < (int)(sizeof(HeadMeta) / 4); i += 32 * kDqWarps)
       reinterpret_cast<uint32_t*>(&ms.m)[i] = reinterpret_cast<const uint32_t*>(a.meta + head)[i];
-    load_dequant_tables(sm + kOffTab, a.dec_image, dtid, 32 * kDqWarps);
+    load_dequant_tables<true>(sm + kOffTab, a.dec_image, dtid, 32 * kDqWarps);
     load_dequant_tables_lo(sm + kOffTab + kDqBytes, a.dec_image, dtid, 32 * kDqWarps);
     asm volatile("bar.sync 4, %0;" ::"n"(32 * kDqWarps) : "memory");
     const uint32_t tab = sb + kOffTab, norms = key_norm_offset(a.kb, a.vb);
@@ -409,9 +409,9 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
         const int t = 2 * j + i;
         if (t >= nt) break;
         const uint32_t row = sb + kOffK + (j & 1) * 2 * kPart + i * 8192;
-        if (code0) keys_by_code(k0, r0k[i], tab, row, true, row + kPart + k0.col, 1024);
+        if (code0) keys_by_code<true>(k0, r0k[i], tab, row, true, row + kPart + k0.col, 1024);
         else keys_by_pair_split(k0, r0k[i], row, kDqBytes, kPart);
-        if (code1) keys_by_code(k1, r1k[i], tab, row, true, row + kPart + k1.col, 1024);
+        if (code1) keys_by_code<true>(k1, r1k[i], tab, row, true, row + kPart + k1.col, 1024);
         else keys_by_pair_split(k1, r1k[i], row, kDqBytes, kPart);
         fetch(t + 2, i);
         read_page(t + 4);
