@@ -274,10 +274,10 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
   cluster.sync();  // nothing of another block is read past this point
   int32_t* kept = a.kept + (int64_t)head * a.kept_stride;
   float* wo = a.w_out ? a.w_out + b * a.wos[0] + h * a.wos[1] : nullptr;
-  uint16_t* list = reinterpret_cast<uint16_t*>(list_space(keys, a.held));  // a round's kept tokens, in order
+  uint16_t* list = reinterpret_cast<uint16_t*>(list_space(keys, a.held));  // a turn's kept tokens, in order
   for (int start = 0; start < n; start += kSelThreads * kPer) {
     const int base = start + tid * kPer;
-    if (n > kSelThreads * kPer) {  // more than one round: this round's classes
+    if (n > kSelThreads * kPer) {  // its classes, where one turn does not take all
       classes(base, stay, at_weight);
       sure = __popc(stay);
       equal = __popc(at_weight);

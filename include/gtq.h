@@ -388,7 +388,9 @@ typedef struct gtq_chunk {
  *             other overlap is not supported.
  *   workspace_dev  workspace_bytes >= gtq_chunk_workspace_bytes(plan, T, n_tokens),
  *             256-byte aligned.  It holds nothing between calls; calls that may
- *             overlap (other streams, graphs replayed at once) need one each.
+ *             overlap (other streams, graphs replayed at once) need one each.  The
+ *             size is that of a call with these T and n_tokens: a smaller call can
+ *             need more, so a workspace for several takes their largest.
  * n_tokens 1 runs the kernel of gtq_decode_attn, whose last bits depend on the order
  * in which its blocks end.  With more, the same call gives the same bits: a score's
  * products are fp16 x fp16 in fp32, and those of the 16 coordinates with the widest
