@@ -36,8 +36,7 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelBins = 2048;
-constexpr int kSelCluster = 16;      // blocks per head at most (2 heads of 524288 tokens: 114 us for the
-                                     // call, 170 with 8; of 131072: 47 with either)
+constexpr int kSelCluster = 16;      // blocks per head at most
 constexpr int kSelTokens = 4096;     // tokens that are worth a block of their own
 constexpr int kPer = 16;             // neighbouring tokens of a thread
 constexpr int kHeld = 32768;         // tokens of a block that stay in shared memory
@@ -554,7 +553,11 @@ cudaError_t launch_evict(const gtq_plan* p, const uint8_t* src, int64_t T, const
   // Blocks for a head: while its tokens are worth them, and no more than one wave of SMs (64 heads
   // of 16384 tokens: 43 us with 4 blocks, 26 with 2; of 32768: 121 with 8, 31 with 2).
   int blocks = 1;
-  while (blocks < kSelCluster && T > (int64_t)blocks * kSelTokens && 2 * blocks * p->n_heads <= p->n_sms) blocks *= 2;
+  while (blocks < 8 && T > (int64_t)blocks * kSelTokens && 2 * blocks * p->n_heads <= p->n_sms) blocks *= 2;
+  // Clusters of 16 have to find 16 SMs close together, and wait longer for one another: for long
+  // sequences of few heads (4 heads of 262144 tokens: 93 us, 109 with 8 blocks; of 70000: 45 and 43;
+  // 8 heads of 262144: 177 and 158).
+  if (blocks == 8 && T > 8 * 4 * (int64_t)kSelTokens && 2 * kSelCluster * p->n_heads <= p->n_sms) blocks = kSelCluster;
   const int64_t stretch = (T + blocks - 1) / blocks + kPer;
   a.held = (int)std::min<int64_t>(stretch, kHeld);
   const size_t sel_smem = (size_t)(a.held + a.held / 16 + 1) * sizeof(uint32_t) +
