@@ -10,7 +10,7 @@
 //   * warps 0-3, 4-7   softmax: thread = row (tensor-memory lane).  Scores are read
 //     from tensor memory, P goes back over them as fp16 and is the A operand of the
 //     second product.  The reference maximum moves only when it grew by more than
-//     2^8: then the row's output in tensor memory is rescaled (by its own threads,
+//     2^4: then the row's output in tensor memory is rescaled (by its own threads,
 //     while no product on it runs).
 //     The first warp of each group of four also issues the group's products, as soon as the
 //     group has written its P: one hand-off less than a warp of its own.
@@ -35,8 +35,11 @@
 // logit comes from coordinates whose part of it is small.  P's sum is taken before P is
 // rounded.  q is scaled by log2(e), so probabilities are powers of 2.  The queries' rotation
 // and the values' way back are products of the same block, with the rotations split into
-// fp16 hi + lo and (for the way back) the output too.  All sums are fp32.  A row comes out
-// within 4e-4 of attention in 64 bits (2-norm), 2e-4 of it the result's own rounding.
+// fp16 hi + lo and (for the way back) the output too.  All sums are fp32.  Rows come out
+// 4e-4 to 5e-4 off attention in 64 bits (2-norm; 2e-4 is the result's own rounding) while logits
+// are of a few units beyond the first 16 coordinates.  Those of larger logits are not: a logit of 15 spread
+// evenly over 128 coordinates is off by 5e-3 at most, and a row that hangs on it by half as much (2.7e-3
+// measured).
 //
 // What bounds it: up to 128 rows, turning codes (about 4000 cycles a step of 128 tokens; 40
 // rows over 2 x 131072 tokens, 3 bits: 60 us for 29 MB).  With pairs, the chain from a step's
@@ -58,7 +61,13 @@ constexpr int kDqWarps = 8;
 constexpr int kChunkThreads = 32 * (kSoftWarps + kDqWarps);
 constexpr int kBlockTok = 128;     // tokens of a step
 constexpr int kSplitSlots = 8;     // slots (pairs of coordinates) with a low part
-constexpr float kRescale = 8.f;    // growth of the maximum (log2) that moves the reference
+// P = 2^(score - ref) is fp16, the row's ref 2^kTop below the maximum that set it, so the largest P
+// lies in [2^kTop, 2^15]: a token keeps P's full precision down to 2^-25 of that maximum, and an
+// absolute 2^-36 of it below.  (One token with .9999 of a row and a hundredth of the others' value, before
+// 16384 of them: rows are off by 6e-4, and by 1.4e-2 with ref at the maximum and kRescale 8.)  kRescale 8, 4, 2, 1: 8192 rows over
+// 2 x 131072 tokens take 1460, 1469, 1481, 1522 us.
+constexpr float kRescale = 4.f;          // growth of the maximum (log2) that moves the reference
+constexpr float kTop = 15.f - kRescale;  // log2 P of a maximum that does
 
 // shared memory, from a 1024-byte boundary
 constexpr uint32_t kQHi = 32768;                    // queries of 128 rows, fp16 (two swizzled atoms)
@@ -393,9 +402,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       const bool whole = __all_sync(0xffffffffu, cnt == kBlockTok);
       if (warp_on) {
         const float mx = whole ? row_max<false>(t_s, cnt) : row_max<true>(t_s, cnt);
-        const bool grow = mx > ref + kRescale;  // also out of -inf
+        const bool grow = mx > ref + (kTop + kRescale);  // also out of -inf
         if (__any_sync(0xffffffffu, grow)) {
-          const float now = grow ? mx : ref;
+          const float now = grow ? mx - kTop : ref;
           const float f = grow ? ex2(ref - now) : 1.f;
           sum *= f;
           ref = now;

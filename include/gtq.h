@@ -394,9 +394,11 @@ typedef struct gtq_chunk {
  * n_tokens 1 runs the kernel of gtq_decode_attn, whose last bits depend on the order
  * in which its blocks end.  With more, the same call gives the same bits: a score's
  * products are fp16 x fp16 in fp32, and those of the 16 coordinates with the widest
- * codes carry the low parts of both factors as well; probabilities enter the second
- * product as fp16; softmax statistics and sums are fp32.  A row with a NaN in its
- * query gets NaNs (n_tokens above 1) and changes no other row.
+ * codes carry the low parts of both factors as well; probabilities and values enter
+ * the second product as fp16 (a token below 2^-25 of the largest weight of its row's
+ * stretch keeps 2^-36 of that weight); softmax statistics and sums are fp32.  Of a
+ * logit, the part beyond those 16 coordinates is good to about 2^-11 of its terms.
+ * A row with a NaN in its query gets NaNs (n_tokens above 1) and changes no other row.
  * Errors: INVALID, UNSUPPORTED (head_dim != 128; a K-only plan), CUDA.
  */
 GTQ_API int gtq_chunk_attn(gtq_plan* plan, const void* packed_dev, int64_t T,
