@@ -42,6 +42,10 @@ constexpr int kPer = 16;             // neighbouring tokens of a thread
 constexpr int kHeld = 32768;         // tokens of a block that stay in shared memory
 constexpr int kMoveThreads = 256;
 constexpr int kMaxBatch = 12;        // source tiles in shared memory at once, at most
+// Dynamic shared memory of a block, at most.  The kernels' limits are set to these and never to a
+// call's own size: a limit belongs to the process, and another thread's call would launch against it.
+constexpr size_t kMaxSelSmem = (kHeld + kHeld / kPer + 1) * sizeof(uint32_t) + kSelThreads * kPer * sizeof(uint16_t);
+constexpr size_t kMaxMoveSmem = 110 * 1024;  // two blocks fit on an SM
 
 struct EvictArgs {
   const float* w;
@@ -562,7 +566,7 @@ cudaError_t launch_evict(const gtq_plan* p, const uint8_t* src, int64_t T, const
   a.held = (int)std::min<int64_t>(stretch, kHeld);
   const size_t sel_smem = (size_t)(a.held + a.held / 16 + 1) * sizeof(uint32_t) +
                           std::min<int64_t>(stretch, kSelThreads * kPer) * sizeof(uint16_t);
-  cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sel_smem);
+  cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSelSmem);
   if (e == cudaSuccess)  // clusters above 8 blocks
     e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
@@ -584,10 +588,10 @@ cudaError_t launch_evict(const gtq_plan* p, const uint8_t* src, int64_t T, const
   // source tiles of a new tile: about T / keep and two cut ones.  More at once cost blocks on an SM
   // (64 heads, a quarter kept: 84 us for the call, 97 with two tiles more); two blocks fit in any case
   const int64_t span = (T + most - 1) / most + 2;
-  const int64_t room = 110 * 1024 / (int64_t)(p->tile_bytes + 16) - 1;
+  const int64_t room = (int64_t)kMaxMoveSmem / (int64_t)(p->tile_bytes + 16) - 1;
   a.batch = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(span, kMaxBatch), room));
   const size_t smem = p->tile_bytes + a.batch * (p->tile_bytes + 16);
-  e = cudaFuncSetAttribute(move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  e = cudaFuncSetAttribute(move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxMoveSmem);
   if (e != cudaSuccess) return e;
   move_kernel<<<dim3((unsigned)((most + kTile - 1) / kTile), (unsigned)p->n_heads), kMoveThreads, smem, s>>>(
       a, p->d_status);
