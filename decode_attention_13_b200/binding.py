@@ -14,12 +14,16 @@ The functions mirror the C ABI in ``include/gtq.h``:
 
 Tensor arguments may be torch tensors (CUDA memory; their data pointer and
 strides are passed through) or raw integer device pointers.
+gtq_rope, gtq_chunk_attn, gtq_attn_weights and gtq_evict refuse (ValueError)
+tensors of another type than their kernels read, and tensors that are not on the
+plan's GPU (gtq_rope: the current one).
 """
 
 from __future__ import annotations
 
 import ctypes
 import os
+import sys
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgtq.so")
@@ -264,6 +268,24 @@ def _stream(s) -> int:
     return int(s.cuda_stream)
 
 
+def _current_device():
+    torch = sys.modules.get("torch")
+    return torch.cuda.current_device() if torch is not None and torch.cuda.is_initialized() else None
+
+
+def _need(x, what: str, device, dtype=None) -> None:
+    """Refuses a tensor of another type, or one that is not on the GPU `device` (None: any)."""
+    if x is None or isinstance(x, int):  # absent, or a raw device pointer
+        return
+    if dtype is not None and x.dtype is not dtype:
+        raise ValueError("%s must be %s, not %s" % (what, str(dtype)[6:], str(x.dtype)[6:]))
+    at = x.get_device()
+    if at < 0:
+        raise ValueError("%s must be on a GPU, not %s" % (what, x.device))
+    if device is not None and at != device:
+        raise ValueError("%s must be on cuda:%d, not %s" % (what, device, x.device))
+
+
 def _strides4(x, strides):
     if strides is not None:
         return (ctypes.c_int64 * 4)(*[int(v) for v in strides])
@@ -274,11 +296,13 @@ def _strides4(x, strides):
 
 
 class Plan:
-    """Owning handle of a gtq_plan (freed by gtq_free or on garbage collection)."""
+    """Owning handle of a gtq_plan (freed by gtq_free or on garbage collection).  device: the index
+    of the GPU it was made on, or None where torch does not know it."""
 
-    def __init__(self, handle: int, cfg: gtq_config):
+    def __init__(self, handle: int, cfg: gtq_config, device=None):
         self.handle = handle
         self.cfg = cfg
+        self.device = _current_device() if device is None else device
 
     @property
     def packed_bytes(self) -> int:
@@ -382,17 +406,19 @@ def gtq_decode_attn_full(plan: Plan, packed, T: int, q, out, layout=None, kv=Non
     _check(rc, "gtq_decode_attn_full")
 
 
-def _rope_tensor(cfg, x, y, batch, tokens, name):
+def _rope_tensor(cfg, x, y, batch, tokens, name, dtype, device):
     shape = x.shape
+    if x.dtype is not dtype or device < 0 or x.get_device() != device:
+        _need(x, name, device, dtype)
     if len(shape) != 4 or shape[3] != cfg.head_dim or shape[0] != batch or shape[2] != tokens:
         raise ValueError("%s must be [%d, heads, %d, %d]" % (name, batch, tokens, cfg.head_dim))
     st = _I64x4(*x.stride())
-    if x.element_size() != (2 if cfg.dtype == DTYPE_FP16 else 4):
-        raise ValueError("%s must have the config's dtype" % name)
     if y is None:
         return gtq_rope_tensor(x.data_ptr(), x.data_ptr(), shape[1], 0, st, st)
-    if y.shape != shape or y.dtype != x.dtype:
-        raise ValueError("%s and its output must have one shape and dtype" % name)
+    if y.dtype is not dtype or y.get_device() != device:
+        _need(y, name + "_out", device, dtype)
+    if y.shape != shape:
+        raise ValueError("%s and its output must have one shape" % name)
     return gtq_rope_tensor(x.data_ptr(), y.data_ptr(), shape[1], 0, st, _I64x4(*y.stride()))
 
 
@@ -404,14 +430,22 @@ def gtq_rope(cfg: gtq_rope_config, q=None, q_out=None, k=None, k_out=None, posit
     first = q if q is not None else k
     if first is None:
         raise ValueError("gtq_rope needs q or k")
-    if first.dim() != 4:
+    shape = first.shape
+    if len(shape) != 4:
         raise ValueError("gtq_rope takes [batch, heads, tokens, head_dim]")
-    batch, _, tokens, _ = first.shape
+    batch, _, tokens, _ = shape
+    import torch
+
+    dtype = torch.float16 if cfg.dtype == DTYPE_FP16 else torch.float32
+    device = first.get_device()
+    if device >= 0 and device != torch.cuda.current_device():
+        raise ValueError("gtq_rope runs on the current device, cuda:%d" % torch.cuda.current_device())
     pos_stride = pos_ptr = 0
     if positions is not None:
         ps = positions.shape
-        if positions.element_size() != 8 or not ps or ps[-1] != tokens or len(ps) > 2 or (
-                len(ps) == 2 and ps[0] != batch):
+        if positions.dtype is not torch.int64 or positions.get_device() != device:
+            _need(positions, "positions", device, torch.int64)
+        if not ps or ps[-1] != tokens or len(ps) > 2 or (len(ps) == 2 and ps[0] != batch):
             raise ValueError("positions must be int64 [batch, tokens] or [tokens]")
         st = positions.stride()
         if tokens > 1 and st[-1] != 1:
@@ -419,25 +453,39 @@ def gtq_rope(cfg: gtq_rope_config, q=None, q_out=None, k=None, k_out=None, posit
         if len(ps) == 2 and batch > 1:
             pos_stride = st[0]
         pos_ptr = positions.data_ptr()
-    tq = None if q is None else ctypes.byref(_rope_tensor(cfg, q, q_out, batch, tokens, "q"))
-    tk = None if k is None else ctypes.byref(_rope_tensor(cfg, k, k_out, batch, tokens, "k"))
+    tq = None if q is None else ctypes.byref(_rope_tensor(cfg, q, q_out, batch, tokens, "q", dtype, device))
+    tk = None if k is None else ctypes.byref(_rope_tensor(cfg, k, k_out, batch, tokens, "k", dtype, device))
     rc = _lib.gtq_rope(ctypes.byref(cfg), batch, tokens, pos_ptr, pos_stride, pos0, tq, tk,
                        _stream(stream))
     if rc != GTQ_OK:
         _check(rc, "gtq_rope")
 
 
-def _chunk(plan, q, out, chunk_lens, causal):
-    c = plan.cfg
-    if q.dim() != 4 or q.element_size() != 2 or q.shape[0] != c.batch or (
-            q.shape[1] != c.n_q_heads or q.shape[3] != c.head_dim):
+def _chunk(plan, q, out, chunk_lens, causal, packed=None, workspace=None):
+    import torch
+
+    c, device = plan.cfg, plan.device
+    if q.dim() != 4 or q.shape[0] != c.batch or q.shape[1] != c.n_q_heads or q.shape[3] != c.head_dim:
         raise ValueError("q must be fp16 [batch, query heads, new tokens, %d]" % c.head_dim)
-    if out is not None and (tuple(out.shape) != tuple(q.shape) or out.dtype != q.dtype):
-        raise ValueError("out must have the shape and type of q")
+    if out is not None and tuple(out.shape) != tuple(q.shape):
+        raise ValueError("out must have the shape of q")
+    _need(q, "q", device, torch.float16)
+    _need(out, "out", device, torch.float16)
+    _lens(chunk_lens, "chunk_lens", plan)
+    _need(packed, "packed", device)
+    _need(workspace, "workspace", device)
     ch = gtq_chunk(int(q.shape[2]), _ptr(chunk_lens) or None, int(bool(causal)), 0)
     ch.q_strides = _live_strides(q)
     ch.out_strides = _live_strides(out if out is not None else q)
     return ch
+
+
+def _lens(x, what, plan):
+    import torch
+
+    _need(x, what, plan.device, torch.int32)
+    if x is not None and not isinstance(x, int) and (x.numel() != plan.cfg.batch or not x.is_contiguous()):
+        raise ValueError("%s must be contiguous int32 [batch]" % what)
 
 
 def _live_strides(x):
@@ -459,7 +507,7 @@ def gtq_chunk_attn(plan: Plan, packed, T: int, q, out, workspace, layout=None, c
                    causal=True, stream=None) -> None:
     """Attention of the new tokens q [batch, query heads, new tokens, 128] (fp16, any strides with
     dense rows) over the cache into out (the same shape)."""
-    ch = _chunk(plan, q, out, chunk_lens, causal)
+    ch = _chunk(plan, q, out, chunk_lens, causal, packed, workspace)
     rc = _lib.gtq_chunk_attn(plan.handle, _ptr(packed), int(T), _lay(layout), ctypes.byref(ch),
                              _ptr(q), _ptr(out), _ptr(workspace), _nbytes(workspace),
                              _stream(stream))
@@ -472,8 +520,11 @@ def gtq_weights_workspace(plan: Plan, T: int, n_tokens: int) -> int:
 
 
 def _weights2(w, plan, what):
-    if w.dim() != 3 or w.element_size() != 4 or tuple(w.shape[:2]) != (plan.cfg.batch, plan.cfg.n_kv_heads):
+    import torch
+
+    if w.dim() != 3 or tuple(w.shape[:2]) != (plan.cfg.batch, plan.cfg.n_kv_heads):
         raise ValueError("%s must be fp32 [batch, kv heads, tokens]" % what)
+    _need(w, what, plan.device, torch.float32)
     if w.shape[2] > 1 and w.stride(2) != 1:
         raise ValueError("%s must be dense along tokens" % what)
     return (ctypes.c_int64 * 2)(int(w.stride(0)), int(w.stride(1)))
@@ -483,7 +534,7 @@ def gtq_attn_weights(plan: Plan, packed, T: int, q, weights_out, workspace, weig
                      layout=None, chunk_lens=None, causal=True, stream=None) -> None:
     """weights_out = weights_in (or 0) + the attention every cached token gets from q; both
     [batch, kv heads, >= T] fp32."""
-    ch = _chunk(plan, q, None, chunk_lens, causal)
+    ch = _chunk(plan, q, None, chunk_lens, causal, packed, workspace)
     st = _weights2(weights_out, plan, "weights_out")
     if weights_out.shape[2] < T or (weights_in is not None and (
             weights_in.shape[2] < T or tuple(_weights2(weights_in, plan, "weights_in")) != tuple(st))):
@@ -505,19 +556,22 @@ def gtq_evict(plan: Plan, packed, T: int, weights, keep: int, dst, new_lens, wor
     """Move the tokens that stay (n_first, n_recent, and the largest weights) into dst.
     weights [batch, kv heads, >= T]; weights_out [batch, kv heads, >= keep]; kept int32
     [batch, kv heads, keep]; new_lens int32 [batch]."""
-    c = plan.cfg
-    if weights.shape[2] < T or (weights_out is not None and weights_out.shape[2] < min(keep, T)):
-        raise ValueError("weights need T tokens, weights_out min(keep, T)")
-    if kept is not None and (tuple(kept.shape) != (c.batch, c.n_kv_heads, keep) or not kept.is_contiguous()
-                             or kept.element_size() != 4):
-        raise ValueError("kept must be contiguous int32 [batch, kv heads, keep]")
-    if new_lens.numel() != c.batch or new_lens.element_size() != 4:
-        raise ValueError("new_lens must be int32 [batch]")
+    import torch
+
+    c, device = plan.cfg, plan.device
     ev = gtq_eviction(int(keep), int(n_first), int(n_recent))
     ev.weights_dev, ev.w_strides = _ptr(weights), _weights2(weights, plan, "weights")
     if weights_out is not None:
         ev.weights_out_dev = _ptr(weights_out)
         ev.w_out_strides = _weights2(weights_out, plan, "weights_out")
+    if weights.shape[2] < T or (weights_out is not None and weights_out.shape[2] < min(keep, T)):
+        raise ValueError("weights need T tokens, weights_out min(keep, T)")
+    _need(kept, "kept", device, torch.int32)
+    if kept is not None and (tuple(kept.shape) != (c.batch, c.n_kv_heads, keep) or not kept.is_contiguous()):
+        raise ValueError("kept must be contiguous int32 [batch, kv heads, keep]")
+    _lens(new_lens, "new_lens", plan)
+    for x, what in ((packed, "packed"), (dst, "dst"), (workspace, "workspace")):
+        _need(x, what, device)
     ev.kept_dev = _ptr(kept) or None
     ev.new_lens_dev = _ptr(new_lens)
     rc = _lib.gtq_evict(plan.handle, _ptr(packed), int(T), _lay(layout), ctypes.byref(ev),
