@@ -22,6 +22,7 @@ plan's GPU (gtq_rope: the current one).
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import sys
 
@@ -170,9 +171,16 @@ class gtq_eviction(ctypes.Structure):
 
 
 def make_rope(head_dim, theta, rotary_dim=None, rope_pairing=PAIRING_HALF, dtype=DTYPE_FP16,
-              scaling=ROPE_PLAIN, factor=1.0, original_context=0.0, low_freq=1.0, high_freq=4.0,
-              magnitude=1.0, backward=False) -> gtq_rope_config:
-    """A gtq_rope_config; rotary_dim defaults to the whole head."""
+              scaling=ROPE_PLAIN, factor=1.0, original_context=0.0, low_freq=1.0, high_freq=None,
+              magnitude=None, backward=False) -> gtq_rope_config:
+    """A gtq_rope_config.  rotary_dim defaults to the whole head; the ramp's turns and the magnitude to
+    what is customary for the scaling: 1 and 4 turns (ROPE_LLAMA3), 1 and 32 turns with the
+    magnitude 0.1 ln(factor) + 1 (ROPE_YARN), and else the magnitude 1."""
+    yarn = scaling == ROPE_YARN
+    if high_freq is None:
+        high_freq = 32.0 if yarn else 4.0
+    if magnitude is None:
+        magnitude = 0.1 * math.log(factor) + 1.0 if yarn and factor > 0 else 1.0
     return gtq_rope_config(head_dim, head_dim if rotary_dim is None else rotary_dim, rope_pairing,
                            dtype, scaling, int(backward), theta, factor, original_context,
                            low_freq, high_freq, magnitude)

@@ -304,6 +304,9 @@ GTQ_API int gtq_decode_attn_full(gtq_plan* plan, const void* packed_dev, int64_t
  *             lo = max(floor(c(high_freq)), 0), hi = min(ceil(c(low_freq)), rotary_dim - 1),
  *             s = clamp((i - lo) / max(hi - lo, 0.001), 0, 1),
  *             f_i <- s f_i / factor + (1 - s) f_i
+ * (customary: LLAMA3 low_freq 1, high_freq 4, magnitude 1; YARN low_freq 1,
+ * high_freq 32, magnitude 0.1 ln(factor) + 1.  Nothing here is filled in: a config
+ * holds what the call uses.)
  * backward = 1 turns by -a: the transposed matrix, i.e. the gradient with respect
  * to x of an output gradient (and, at magnitude 1, the inverse).
  */
