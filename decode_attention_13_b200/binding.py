@@ -14,6 +14,10 @@ The functions mirror the C ABI in ``include/gtq.h``:
 
 Tensor arguments may be torch tensors (CUDA memory; their data pointer and
 strides are passed through) or raw integer device pointers.
+A call runs on `stream` (a torch stream or a raw handle).  stream=None is CUDA's
+legacy default stream, not torch's current one: under `torch.cuda.stream(s)` pass
+stream=s, or the call is not ordered with what torch does on s.
+
 gtq_rope, gtq_chunk_attn, gtq_attn_weights and gtq_evict refuse (ValueError)
 tensors of another type than their kernels read, and tensors that are not on the
 plan's GPU (gtq_rope: the current one).
@@ -434,7 +438,7 @@ def gtq_rope(cfg: gtq_rope_config, q=None, q_out=None, k=None, k_out=None, posit
              stream=None) -> None:
     """Rotate q and / or k ([batch, heads, tokens, head_dim], any strides with a dense last dim)
     into q_out / k_out (None: in place).  positions: int64 [batch, tokens] or [tokens], or None:
-    pos0 + token."""
+    pos0 + token.  stream: None is the legacy default stream, not torch's current one."""
     first = q if q is not None else k
     if first is None:
         raise ValueError("gtq_rope needs q or k")
@@ -514,7 +518,8 @@ def gtq_chunk_workspace(plan: Plan, T: int, n_tokens: int) -> int:
 def gtq_chunk_attn(plan: Plan, packed, T: int, q, out, workspace, layout=None, chunk_lens=None,
                    causal=True, stream=None) -> None:
     """Attention of the new tokens q [batch, query heads, new tokens, 128] (fp16, any strides with
-    dense rows) over the cache into out (the same shape)."""
+    dense rows) over the cache into out (the same shape).  stream: None is the legacy default
+    stream, not torch's current one."""
     ch = _chunk(plan, q, out, chunk_lens, causal, packed, workspace)
     rc = _lib.gtq_chunk_attn(plan.handle, _ptr(packed), int(T), _lay(layout), ctypes.byref(ch),
                              _ptr(q), _ptr(out), _ptr(workspace), _nbytes(workspace),
@@ -541,7 +546,8 @@ def _weights2(w, plan, what):
 def gtq_attn_weights(plan: Plan, packed, T: int, q, weights_out, workspace, weights_in=None,
                      layout=None, chunk_lens=None, causal=True, stream=None) -> None:
     """weights_out = weights_in (or 0) + the attention every cached token gets from q; both
-    [batch, kv heads, >= T] fp32."""
+    [batch, kv heads, >= T] fp32.  stream: None is the legacy default stream, not torch's current
+    one."""
     ch = _chunk(plan, q, None, chunk_lens, causal, packed, workspace)
     st = _weights2(weights_out, plan, "weights_out")
     if weights_out.shape[2] < T or (weights_in is not None and (
@@ -563,7 +569,8 @@ def gtq_evict(plan: Plan, packed, T: int, weights, keep: int, dst, new_lens, wor
               stream=None) -> None:
     """Move the tokens that stay (n_first, n_recent, and the largest weights) into dst.
     weights [batch, kv heads, >= T]; weights_out [batch, kv heads, >= keep]; kept int32
-    [batch, kv heads, keep]; new_lens int32 [batch]."""
+    [batch, kv heads, keep]; new_lens int32 [batch].  stream: None is the legacy default stream,
+    not torch's current one."""
     import torch
 
     c, device = plan.cfg, plan.device
