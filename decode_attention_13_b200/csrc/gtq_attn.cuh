@@ -1,6 +1,7 @@
 // What the kernels over several new tokens of a sequence share.
 #pragma once
 
+#include "gtq_dequant.cuh"
 #include "gtq_internal.h"
 #include "gtq_tc.cuh"
 
@@ -77,12 +78,14 @@ __device__ __forceinline__ void put_query_row(uint8_t* operand, int row, const u
     *reinterpret_cast<uint4*>(o + (c >> 3) * 16384 + (((c & 7) ^ sw) << 4)) = v;
   }
 }
-// 8 values, scaled and kept in the fp16 range, as fp16 hi and the rest.
+// 8 values, scaled, as fp16 hi and the rest.  An infinity becomes a NaN, as it would in a softmax.
 __device__ __forceinline__ void split8(const uint32_t* r, const float* scale, uint4& hi, uint4& lo) {
   uint32_t h[4], l[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float x = __uint_as_float(r[2 * e]) * scale[2 * e], y = __uint_as_float(r[2 * e + 1]) * scale[2 * e + 1];
+    float x = __uint_as_float(r[2 * e]) * scale[2 * e], y = __uint_as_float(r[2 * e + 1]) * scale[2 * e + 1];
+    x += x - x;
+    y += y - y;
     asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(h[e]) : "f"(y), "f"(x));
     const __half2 hh = *reinterpret_cast<__half2*>(&h[e]);
     asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(l[e]) : "f"(y - __high2float(hh)), "f"(x - __low2float(hh)));
@@ -90,9 +93,11 @@ __device__ __forceinline__ void split8(const uint32_t* r, const float* scale, ui
   hi = make_uint4(h[0], h[1], h[2], h[3]);
   lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
-// Factor of a rotated query coordinate: log2(e) / (sqrt(d) sqrt(m)), and the keys' 1 / 16 undone.
+// Factor of a rotated query coordinate: log2(e) / (sqrt(d) sqrt(m)), and the keys' kElement undone:
+// 1.02 / sqrt(m).  A coordinate is at most sqrt(m) times the group's root mean square, so hi stays
+// in the fp16 range (split8 would clip it) up to a root mean square of .98 of fp16's largest number.
 __device__ __forceinline__ float query_scale(const HeadMeta& m, int pos) {
-  return (pos >> 1) < m.n_slots ? 16.f * kLog2e * 0.08838834764831845f * m.inv_sqrt_m[m.slot_group[pos >> 1]] : 0.f;
+  return (pos >> 1) < m.n_slots ? kLog2e * 0.08838834764831845f / kElement * m.inv_sqrt_m[m.slot_group[pos >> 1]] : 0.f;
 }
 // k-step ks (16 columns) of a swizzled operand of 128 rows: what its descriptor moves by
 __device__ __forceinline__ uint64_t kstep(uint32_t ks) {

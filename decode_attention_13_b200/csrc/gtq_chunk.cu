@@ -471,8 +471,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const __grid_co
       }
     }
     if (NQ == 2 || grp == 0) {
-      // 16 / sqrt(128): the values' factor (a row with a NaN in its query has a NaN here)
-      const float inv = total == 0.f ? 0.f : 1.4142135623730951f / total;
+      // the values' factor (a row with a NaN in its query has a NaN here)
+      const float inv = total == 0.f ? 0.f : 0.08838834764831845f / kElement / total;
       const float f0 = inv * own, f1 = inv * other;
       const bool two = NQ == 1 && nb > 1;
       uint8_t* ohi = sm + M::qhi + tile * kQHi + lrow * 128;

@@ -8,12 +8,13 @@
 // different banks.  Values: rows = rotated dims, columns = the tile's 64 tokens, one
 // swizzled atom; a warp takes 16 dims, a lane two of them for 16 tokens.
 //
-// An element is cb[code] / 16 * norm: the power of two keeps the largest norm
-// (65504) times the largest centroid in the fp16 range, and is undone in the
-// queries and at the end.  Where low parts have to hold to their last bits (FINE), the
-// codebook's stay as they are and take norm / 16 instead: a 16th of most of them is an fp16
-// subnormal.  (Not where other roundings to fp16 stand beside them: it costs a chunk 1.5% of its
-// time.)
+// An element is cb[code] / 8 * norm, the factor undone in the queries and at the end.  It shares
+// out fp16's range: the largest norm (65504) times the largest centroid (4.61) stays within it,
+// and so does a query's coordinate (query_scale).  fp16 ends at 2^-24, so an element is good to 2^-25
+// at best: that counts where all norms of a head are small, below about 2^-8 for one fp16 an element
+// and below about 1 for two.  Where low parts have to hold to their last bits (FINE), the codebook's
+// stay as they are and take norm / 8 instead: an 8th of them is an fp16 subnormal, off by up to 2^-22 of
+// the norm.  (Not where other roundings to fp16 stand beside them: it costs a chunk 1.5% of its time.)
 //
 // Keys of widths up to 4 take a pair of codes in one lookup, every lane by its own
 // width (mask, table, multiplier), so that four slots of different widths run as
@@ -28,7 +29,9 @@
 
 namespace gtq {
 
-// Lookup tables in shared memory (fp16 values of the codebook / 16): pair tables of
+constexpr float kElement = 0.125f;  // an operand's element: this times cb[code] times norm
+
+// Lookup tables in shared memory (fp16 values of the codebook / 8): pair tables of
 // widths 3, 2, 1 with a copy per lane, as they lie in the decode image (kTabP32W3
 // .. kTabS32W5), a pair table of width 4 in one copy, single codes of all widths
 // (kTabSS: hi | lo << 16; FINE: the low parts not divided), and a zero.
@@ -50,11 +53,11 @@ __device__ __forceinline__ void load_dequant_tables(uint8_t* tab, const uint4* i
   const uint8_t* img = reinterpret_cast<const uint8_t*>(image);
   const uint32_t* ss = reinterpret_cast<const uint32_t*>(img + kTabSS);
   const uint32_t* pp = reinterpret_cast<const uint32_t*>(img + kTabP32W3);
-  auto scaled = [](uint32_t v) { return as_u32(__hmul2(as_h2(v), __float2half2_rn(0.0625f))); };
+  auto scaled = [](uint32_t v) { return as_u32(__hmul2(as_h2(v), __float2half2_rn(kElement))); };
   for (int i = tid; i < (int)(kDqPairBytes / 4); i += n_threads)
     reinterpret_cast<uint32_t*>(tab + kDqPairs)[i] = scaled(pp[i]);
   for (int i = tid; i < 512; i += n_threads)
-    reinterpret_cast<uint32_t*>(tab + kDqSingles)[i] = as_u32(__hmul2(as_h2(ss[i]), __floats2half2_rn(0.0625f, FINE ? 1.f : 0.0625f)));
+    reinterpret_cast<uint32_t*>(tab + kDqSingles)[i] = as_u32(__hmul2(as_h2(ss[i]), __floats2half2_rn(kElement, FINE ? 1.f : kElement)));
   for (int i = tid; i < 256; i += n_threads)
     reinterpret_cast<uint32_t*>(tab + kDqPair4)[i] =
         scaled(__byte_perm(ss[kSingleOff(4) / 4 + (i & 15)], ss[kSingleOff(4) / 4 + (i >> 4)], 0x5410));
@@ -206,7 +209,7 @@ __device__ __forceinline__ void keys_by_pair_split(const KeyLane& k, const KeyRa
   x[0] = __funnelshift_r(r.x[0], r.x[1], odd);
   x[1] = __funnelshift_rc(x[0], r.x[1] >> odd, 4 * w2);
   const uint32_t nw[4] = {r.n.x, r.n.y, r.n.z, r.n.w};
-  const __half2 sixteenth = __float2half2_rn(0.0625f);
+  const __half2 eighth = __float2half2_rn(kElement);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     uint32_t v[4], l[4];
@@ -224,7 +227,7 @@ __device__ __forceinline__ void keys_by_pair_split(const KeyLane& k, const KeyRa
       const __half2 p = __hmul2(as_h2(v[u]), nn);
       sts32(d + 1024 * u, as_u32(p));
       sts32(d + 1024 * u + lo_dst,
-            as_u32(__hfma2(as_h2(l[u]), __hmul2(nn, sixteenth), __hfma2(as_h2(v[u]), nn, __hneg2(p)))));
+            as_u32(__hfma2(as_h2(l[u]), __hmul2(nn, eighth), __hfma2(as_h2(v[u]), nn, __hneg2(p)))));
     }
   }
 }
@@ -270,7 +273,7 @@ __device__ __forceinline__ void keys_by_code(const KeyLane& k, const KeyRaw& r, 
       // hi * n - fp16(hi * n) is exact in one fma (above the subnormals); lo * n joins it
       if (low)
         sts32(dl + (4 * half + u) * lo_rows,
-              as_u32(__hfma2(lo, FINE ? __hmul2(nn, __float2half2_rn(0.0625f)) : nn, __hfma2(hi, nn, __hneg2(p)))));
+              as_u32(__hfma2(lo, FINE ? __hmul2(nn, __float2half2_rn(kElement)) : nn, __hfma2(hi, nn, __hneg2(p)))));
     }
   }
 }

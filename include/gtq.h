@@ -401,7 +401,8 @@ typedef struct gtq_chunk {
  * the second product as fp16 (a token below 2^-25 of the largest weight of its row's
  * stretch keeps 2^-36 of that weight); softmax statistics and sums are fp32.  Of a
  * logit, the part beyond those 16 coordinates is good to about 2^-11 of its terms.
- * A row with a NaN in its query gets NaNs (n_tokens above 1) and changes no other row.
+ * A row with a NaN or an infinity in its query gets NaNs (n_tokens above 1) and changes
+ * no other row.
  * Errors: INVALID, UNSUPPORTED (head_dim != 128; a K-only plan), CUDA.
  */
 GTQ_API int gtq_chunk_attn(gtq_plan* plan, const void* packed_dev, int64_t T,
@@ -424,7 +425,9 @@ GTQ_API size_t gtq_chunk_workspace_bytes(const gtq_plan* plan, int64_t T, int64_
  *                    workspace_bytes >= gtq_weights_workspace_bytes(...) (up to 16 rows
  *                    of a KV head, it holds their fp32 scores).
  * Sums run in a fixed order: the same call gives the same bits.  Scores are
- * exact to about 2^-21 of the largest product.  K-only plans are supported.
+ * exact to about 2^-21 of the largest product, or of the query's largest coordinate
+ * where a head's key norms are all below 1.  NaNs and infinities in a query make the
+ * weights of all tokens that its row sees NaNs.  K-only plans are supported.
  * Errors: INVALID, UNSUPPORTED (head_dim != 128), CUDA.
  */
 GTQ_API int gtq_attn_weights(gtq_plan* plan, const void* packed_dev, int64_t T,

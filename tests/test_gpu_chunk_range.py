@@ -7,8 +7,8 @@ torch = pytest.importorskip("torch")
 
 import decode_attention_13_b200 as gtq  # noqa: E402
 from tests import layout  # noqa: E402
-from tests.serving import Cache, workspace  # noqa: E402
-from tests.test_gpu_chunk import CHUNK_REL_L2  # noqa: E402
+from tests.serving import Cache, probabilities, workspace  # noqa: E402
+from tests.test_gpu_chunk import CHUNK_REL_L2, run_chunk  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +62,72 @@ def test_a_sink_of_small_value_before_a_long_context(n, mass):
         ref, got = p @ V, out[b, hs][:, rows].double().cpu().numpy()
         e = np.linalg.norm(got - ref, axis=-1) / np.linalg.norm(ref, axis=-1)
         assert e.max() <= CHUNK_REL_L2, (b, h, p[..., 0].mean(), e.max())
+
+
+def weights_of(c, q, n):
+    w = torch.zeros((c.B, c.hkv, c.cap), device="cuda")
+    gtq.gtq_attn_weights(c.plan, c.packed, c.cap, q, w, workspace(gtq.gtq_weights_workspace(c.plan, c.cap, n)),
+                         layout=c.layout)
+    torch.cuda.synchronize()
+    assert gtq.gtq_status(c.plan) == gtq.GTQ_OK
+    return w
+
+
+@pytest.mark.parametrize("n", [3, 20, 40, 90])
+@pytest.mark.parametrize("size", [2e4, 6e4])
+def test_queries_near_the_end_of_fp16(n, size):
+    # one group's turned query has nearly all of its length in one coordinate: entries of +-size, signed like a row of the
+    # group's rotation.  The keys are so small that logits stay mild
+    from oracle import allocation, rotation
+
+    c = Cache([300], 1, 8, 3, 3, seed=5, scale=1e-3)
+    group = max(allocation.groups(c.bits[0, 0], 128, 0), key=lambda g: g.m)
+    R = rotation.key_rotation(group.m)
+    q = np.zeros((1, 8, n, 128))
+    rows = np.random.default_rng(n).integers(0, group.m, (8, n))
+    q[0][..., list(group.coords)] = np.where(R[rows] < 0, -size, size)
+    K, V = c.K[0][0], c.V[0][0]
+    # (the most that a logit varies by, brought to 4)
+    spread = np.abs(q[0] @ K.T).max() / np.sqrt(128.0)
+    c = Cache([300], 1, 8, 3, 3, seed=5, scale=1e-3 * 4.0 / spread)
+    assert group == max(allocation.groups(c.bits[0, 0], 128, 0), key=lambda g: g.m)
+    K, V = c.K[0][0], c.V[0][0]
+    qd = torch.from_numpy(q.astype(np.float16)).cuda()
+    p = probabilities(q[0], K, n, True)
+    # A coordinate's term: half a step, 2^-11, for the query, the centroid and the element each, and 2^-25 of the element's
+    # unit, 8 / sqrt(m), for an element (and its centroid's 2^-25 an eighth of the norm at most) among the subnormals
+    off = 0.0
+    for g in allocation.groups(c.bits[0, 0], 128, 0):
+        turned = np.abs(q[0][..., list(g.coords)] @ rotation.key_rotation(g.m).T)
+        k = np.abs(K[:, list(g.coords)] @ rotation.key_rotation(g.m).T)
+        norm = np.linalg.norm(K[:, list(g.coords)], axis=-1).max()
+        off = off + (3 * 2.0 ** -11 * turned @ k.T + (2.0 ** -25 * 8.0 / np.sqrt(g.m) * (1 + norm)) * turned.sum(-1)[..., None])
+    off = (off / np.sqrt(128.0)).max()      # of any logit, in nats; a weight changes by twice that, relatively
+    out = run_chunk(c, qd, n, None, True)
+    ref, got = p @ V, out[0].double().cpu().numpy()
+    e = np.linalg.norm(got - ref, axis=-1)
+    most = np.linalg.norm(V, axis=-1).max()
+    assert np.all(e <= CHUNK_REL_L2 * np.linalg.norm(ref, axis=-1) + np.expm1(2 * off) * most), (off, e.max())
+    w = weights_of(c, qd, n)[0, 0].double().cpu().numpy()
+    sums = p.sum((0, 1))
+    assert np.all(np.abs(w - sums) <= np.expm1(2 * off) * sums + 1e-5 * sums.max()), off
+
+
+@pytest.mark.parametrize("n", [3, 20, 40, 90])     # each form of the kernel; 9000 tokens are split, 200 are not
+@pytest.mark.parametrize("length", [200, 9000])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_infinite_queries_stay_in_their_rows(n, length, sign):
+    c = Cache([length], 1, 8, 3, 3, seed=n)
+    q = c.queries(n, seed=n)
+    want, weights = run_chunk(c, q, n, None, True), weights_of(c, q, n)
+    for dim in (0, 77, 127):
+        bad = q.clone()
+        bad[0, 5, n // 2, dim] = sign * float("inf")
+        got = run_chunk(c, bad, n, None, True)
+        assert bool(got[0, 5, n // 2].isnan().all())
+        got[0, 5, n // 2] = want[0, 5, n // 2]
+        assert torch.equal(got, want)
+        seen = length - n + n // 2 + 1
+        w = weights_of(c, bad, n)
+        assert bool(w[0, 0, :seen].isnan().all())
+        assert torch.equal(w[0, 0, seen:], weights[0, 0, seen:])
