@@ -6,8 +6,9 @@
 // takes kTok positions of one sequence and all heads of q and k, so an angle's
 // sine and cosine are formed once per (position, pair) and used by every head.
 //   * Angles in turns: u = p (f_i / 2 pi) in fp64, reduced by u - rint(u) (exact),
-//     then sincospif of the fp32 rest: the angle is off by at most 2^-25 of a half
-//     turn however far the position.
+//     then sincospif of the fp32 rest, off by 2^-25 of a half turn.  The frequency and
+//     the product are off by a few 2^-53, relatively: p f_i 2^-50 of angle at most,
+//     2^-25 of a half turn at positions of about 2^27.
 //   * An item is two vectors of V elements, the halves of V pairs (HALF: V dims
 //     and the V dims rotary_dim / 2 further; INTERLEAVED: 2 V neighbours) or, past
 //     rotary_dim, one vector that is copied.  An item reads all it needs before it

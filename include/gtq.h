@@ -295,7 +295,8 @@ GTQ_API int gtq_decode_attn_full(gtq_plan* plan, const void* packed_dev, int64_t
  *     y0 = magnitude (x0 cos a - x1 sin a),  y1 = magnitude (x1 cos a + x0 sin a)
  * HALF pairs dims (i, i + rotary_dim / 2), INTERLEAVED (2i, 2i + 1); dims from
  * rotary_dim on are copied.  Angles are formed in fp64 and reduced to one turn
- * before their sine and cosine (exact to 2^-23 at any position below 2^53).
+ * before their sine and cosine: off by at most 2^-23 + p f_i 2^-50 (positions of up to
+ * 2^53 are exact in fp64; the second part passes the first from p f_i = 2^27 on).
  * Scaling for contexts longer than original_context: with n_i = original_context
  * f_i / (2 pi) the turns a pair makes over it,
  *     LLAMA3  s = clamp((n_i - low_freq) / (high_freq - low_freq), 0, 1),
