@@ -31,21 +31,23 @@
 //
 // Roundings.  fp16, half a step 2^-11: the turned keys, P, the values, the result.  Scores:
 // q (hi) k (hi) over all 128 coordinates, plus q (lo) k (hi) and q (hi) k (lo) over
-// the first 16, the widest codes, which carry most of a logit: the error that is left in a
+// the first 16, the widest codes, which carry most of a logit (lo of a key is good to 2^-22 of its
+// group's norm): the error that is left in a
 // logit comes from coordinates whose part of it is small.  P's sum is taken before P is
 // rounded.  q is scaled by log2(e), so probabilities are powers of 2.  The queries' rotation
 // and the values' way back are products of the same block, with the rotations split into
 // fp16 hi + lo and (for the way back) the output too.  All sums are fp32.  Rows come out
-// 4e-4 to 5e-4 off attention in 64 bits (2-norm; 2e-4 is the result's own rounding) while logits
-// are of a few units beyond the first 16 coordinates.  Those of larger logits are not: a logit of 15 spread
-// evenly over 128 coordinates is off by 5e-3 at most, and a row that hangs on it by half as much (2.7e-3
-// measured).
+// 2.8e-4 to 4.1e-4 off attention in 64 bits (2-norm): the result's own rounding is 2e-4 of it, P's
+// and the values' two (centroid, element) are 2e-4 each, independent of one another.  That holds while
+// the logits' parts beyond the first 16 coordinates are of a few units.  A logit of 15 spread evenly over 128
+// coordinates is off by up to 5e-3, and a row that hangs on it by half as much (2.7e-3 measured).
 //
 // What bounds it: up to 128 rows, turning codes (about 4000 cycles a step of 128 tokens; 40
-// rows over 2 x 131072 tokens, 3 bits: 60 us for 29 MB).  With pairs, the chain from a step's
-// scores over the softmax and P to its products, about 5200 cycles a step against 2300 of
-// tcgen05.mma: 8192 rows over 2 x 131072 tokens, 3 bits, take 1.44 ms (0.76 PFLOP/s), 4000
-// rows over 8 x 32768, 2 bits, 0.74 ms (0.72 PFLOP/s).
+// rows over 2 x 131072 tokens, 3 bits, 29 MB: 57 us back to back, 66 us a call on inputs that the
+// L2 cache does not hold).  With pairs, the chain from a step's scores over the softmax and P to its
+// products, about 5200 cycles a step against 2300 of tcgen05.mma: 8192 rows over 2 x 131072 tokens,
+// 3 bits, take 1.44 ms back to back (0.76 PFLOP/s), 4000 rows over 8 x 32768, 2 bits, 0.75 ms (0.72
+// PFLOP/s).
 #include <algorithm>
 
 #include "gtq_attn.cuh"
@@ -842,9 +844,12 @@ Cut cut_of(const gtq_plan* p, int64_t T, int64_t n) {
   Cut c;
   const int64_t rows = n * p->g_q;
   // Up to 128 rows, one tile of them (16 rows over 2 x 131072 tokens: 60 us against 66 with a second,
-  // empty one).  Pairs, where they do not have more rows to fill up: 8 heads of 4096 rows over 32768
-  // tokens take 742 us against 794 at 2 bits (paged; 744 against 863 at 4, 774 against 735 at 3 not
-  // paged), but 768 rows, which would be 1024, 224 against 169.
+  // empty one).  Pairs, where they do not have more rows to fill up: 768 rows, which would be 1024,
+  // take 224 us against 169.  8 heads of 4096 rows over 32768 tokens, with pairs and without, at 2, 3
+  // and 4 bits: paged 751 and 822, 751 and 792, 748 and 860 us; contiguous 775 and 779, 781 and 754, 753
+  // and 826.  Contiguous caches at 3 bits are the one case that loses (2 heads of 8192 rows over 131072
+  // tokens: 1445 and 1421); why a contiguous cache takes longer than a paged one is not known, so
+  // the rule does not go by it.
   const int64_t tiles = (rows + 255) / 256;
   c.nq = rows > 128 ? 2 : 1;
   c.pair = tiles > 1 && 24 * (tiles + (tiles & 1)) <= 25 * tiles;

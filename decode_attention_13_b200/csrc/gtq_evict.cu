@@ -9,7 +9,8 @@
 // counts the digits of its stretch and adds up its share of the digits over the cluster
 // (distributed shared memory), and every block finds the digit where the count from the
 // top passes what is still wanted, in the one share that holds it (2 heads of 131072
-// tokens: 47 us for the call, 51 where every block read all counts).  Then each thread counts 16 neighbouring tokens, one prefix sum
+// tokens, calls back to back: 46 us, and 50 where every block reads all counts; 51 to 53 a call on
+// inputs that the L2 cache does not hold).  Then each thread counts 16 neighbouring tokens, one prefix sum
 // gives it its place, and it writes the indices of those that stay: tokens above that
 // weight, and as many with exactly that weight, lowest index first, as are missing.
 // Bound by the latencies of its dozen block- and cluster-wide steps: 26 us for 64 heads of

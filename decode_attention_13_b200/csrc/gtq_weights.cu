@@ -17,13 +17,14 @@
 //
 // With up to kKeepRows rows of a KV head, pass 0 leaves the scores themselves (4 bytes a row
 // and token) and kept_kernel takes the place of pass 1: writing and reading them costs less than
-// turning the codes into operands again (2 heads of 131072 tokens: 8 rows 50 us against 69, 16
-// rows 60 against 70, 24 rows 72 against 70, 64 rows 138 against 73).
+// turning the codes into operands again.  Kept and turned again, us back to back, at 8, 16, 24 and 32
+// rows: 2 heads of 131072 tokens 48 66, 58 67, 70 67, 81 68; 8 of 32768 47 66, 53 66, 61 67, 70 67; 64 of
+// 16384 161 233, 181 233, 209 236, 245 236; 32 of 8192 48 69, 53 69, 60 70, 69 70.
 // Rows beyond 128 of a KV head are more blocks, whose sums lie side by side in the
 // workspace until add_kernel joins them in order.
 //
 // Bound by turning codes into operands, as chunks of few rows are: both passes read the keys'
-// codes and norms, 18 MB over 2 x 131072 tokens at 3 bits (50 us for 8 rows), 13 MB over
+// codes and norms, 18 MB over 2 x 131072 tokens at 3 bits (51 us for 8 rows), 13 MB over
 // 8 x 32768 at 2 bits (128 rows: 76 us).  A pair of codes is one lookup for hi and one for lo,
 // and each tile of a step has registers of its own, filled a step ahead: code by code and a tile
 // ahead took 53 and 80 us.

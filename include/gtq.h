@@ -391,14 +391,16 @@ typedef struct gtq_chunk {
  *             that sees no token gets zeros.  out may be q with the same strides; any
  *             other overlap is not supported.
  *   workspace_dev  workspace_bytes >= gtq_chunk_workspace_bytes(plan, T, n_tokens),
- *             256-byte aligned.  It holds nothing between calls; calls that may
+ *             256-byte aligned (520 bytes for each row and part of the tokens, where
+ *             a call is split over them).  It holds nothing between calls; calls that may
  *             overlap (other streams, graphs replayed at once) need one each.  The
  *             size is that of a call with these T and n_tokens: a smaller call can
  *             need more, so a workspace for several takes their largest.
  * n_tokens 1 runs the kernel of gtq_decode_attn, whose last bits depend on the order
  * in which its blocks end.  With more, the same call gives the same bits: a score's
  * products are fp16 x fp16 in fp32, and those of the 16 coordinates with the widest
- * codes carry the low parts of both factors as well; probabilities and values enter
+ * codes carry the low parts of both factors as well (the keys' to 2^-22 of a group's
+ * norm); probabilities and values enter
  * the second product as fp16 (a token below 2^-25 of the largest weight of its row's
  * stretch keeps 2^-36 of that weight); softmax statistics and sums are fp32.  Of a
  * logit, the part beyond those 16 coordinates is good to about 2^-11 of its terms.
@@ -423,8 +425,13 @@ GTQ_API size_t gtq_chunk_workspace_bytes(const gtq_plan* plan, int64_t T, int64_
  *   weights_out_dev  fp32, the same strides (not negative, 0 only for an extent of 1);
  *                    elements t >= len_b are left as they are.
  *   others           as gtq_chunk_attn (out_strides are not read);
- *                    workspace_bytes >= gtq_weights_workspace_bytes(...) (up to 16 rows
- *                    of a KV head, it holds their fp32 scores).
+ *                    workspace_bytes >= gtq_weights_workspace_bytes(...).  With r rows of
+ *                    a KV head (n_tokens x query heads a KV head) it holds, for each of
+ *                    the T tokens and KV heads, 4 r bytes (r <= 16) or 4 ceil(r / 128)
+ *                    (r > 128), and 8 bytes for each row and part of the tokens.  Over a
+ *                    long prompt that is more than the cache (8192 rows: 256 bytes a
+ *                    token): call in pieces of new tokens, with weights_in, or over the
+ *                    last ones only.
  * Sums run in a fixed order: the same call gives the same bits.  Scores are
  * exact to about 2^-21 of the largest product, or of the query's largest coordinate
  * where a head's key norms are all below 1.  NaNs and infinities in a query make the
@@ -465,7 +472,8 @@ typedef struct gtq_eviction {
  * gtq_evict -- move the tokens that stay into another cache of the same plan.
  *   src_dev, T, lay  the cache as gtq_decode_attn_ex reads it.
  *   dst_dev          the new cache, 16-byte aligned, dst_bytes as packed_bytes of
- *                    gtq_quantize_pack_ex; tiles below ceil(min(len_b, keep) / 64)
+ *                    gtq_quantize_pack_ex: a contiguous one has room for the plan's whole
+ *                    capacity, so only paged caches free memory; tiles below ceil(min(len_b, keep) / 64)
  *                    are written in full (bits of tokens behind the last, and norms
  *                    of groups a head does not have, are 0), others not at all.
  *   dst_lay          NULL (contiguous) or a layout whose block table names the new
