@@ -8,7 +8,7 @@ torch = pytest.importorskip("torch")
 import decode_attention_13_b200 as gtq  # noqa: E402
 from tests import layout  # noqa: E402
 from tests.serving import Cache, probabilities, workspace  # noqa: E402
-from tests.test_gpu_chunk import CHUNK_REL_L2, run_chunk  # noqa: E402
+from tests.test_gpu_chunk import CHUNK_REL_L2, run_chunk, same  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -131,3 +131,53 @@ def test_infinite_queries_stay_in_their_rows(n, length, sign):
         w = weights_of(c, bad, n)
         assert bool(w[0, 0, :seen].isnan().all())
         assert torch.equal(w[0, 0, seen:], weights[0, 0, seen:])
+
+
+@pytest.mark.parametrize("n", [1, 2])      # 8 and 16 rows: weights come from kept scores, one token from the decode kernel
+@pytest.mark.parametrize("length", [200, 9000])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_odd_queries_of_few_rows(n, length, value):
+    c = Cache([length], 1, 8, 3, 3, seed=1)
+    q = c.queries(n, seed=n)
+    want, weights = run_chunk(c, q, n, None, True), weights_of(c, q, n)
+    bad = q.clone()
+    bad[0, 5, 0, 77] = value
+    got, w, seen = run_chunk(c, bad, n, None, True), weights_of(c, bad, n), length - n + 1
+    assert bool(w[0, 0, :seen].isnan().all()) and torch.equal(w[0, 0, seen:], weights[0, 0, seen:])
+    if n > 1:
+        assert bool(got[0, 5, 0].isnan().all())
+    got[0, 5, 0] = want[0, 5, 0]
+    assert same(got, want, n, c)
+
+
+@pytest.mark.parametrize("n", [20, 100, 250])
+@pytest.mark.parametrize("growth", [1.0, 2.0, 3.9, 4.1, 6.0])     # of the logits from one step of 128 tokens to the next, log2
+def test_logits_that_grow_along_the_context(n, growth):
+    # the reference maximum stays for some steps and moves at others, while the old tokens' weights fade.  The logits stand
+    # in two RoPE blocks, whose low parts are kept: 35 log2 at most, off by 2^-20 of that
+    B, hkv, gq, T = 4, 37, 2, 1024    # (enough heads that no call is split over the tokens)
+    rng = np.random.default_rng(n)
+    loud = [3, 67, 20, 84]
+    u = np.zeros(128)
+    u[loud] = 0.5
+    ramp = np.minimum(growth * np.arange(T) / 128.0, 35.0) * np.log(2.0)
+    k = 0.02 * rng.standard_normal((B, hkv, T, 128)) + (ramp * np.sqrt(128.0) / 8.0)[None, None, :, None] * u
+    v = rng.standard_normal((B, hkv, T, 128))
+    q = 8.0 * u + 0.05 * rng.standard_normal((B, hkv * gq, n, 128))
+    q, k, v = (torch.from_numpy(x.astype(np.float16)).cuda() for x in (q, k, v))
+    plan = gtq.gtq_alloc_bits(gtq.make_config(B, hkv * gq, hkv, 4, 4, T), k, T)
+    packed = torch.empty(plan.packed_bytes, dtype=torch.uint8, device="cuda")
+    gtq.gtq_quantize_pack(plan, k, v, 0, T, packed)
+    out = torch.empty_like(q)
+    need = gtq.gtq_chunk_workspace(plan, T, n)
+    assert need == 256, "the call is split"
+    gtq.gtq_chunk_attn(plan, packed, T, q, out, workspace(need))
+    torch.cuda.synchronize()
+    assert gtq.gtq_status(plan) == gtq.GTQ_OK
+    for b, h in ((0, 0), (3, 36)):
+        K, V = Head(plan, hkv, 4, 4, T // 64).dequantised(packed, None, b, h, T)
+        hs = slice(h * gq, (h + 1) * gq)
+        ref = probabilities(q[b, hs].float().cpu().numpy(), K, n, True) @ V
+        got = out[b, hs].double().cpu().numpy()
+        e = np.linalg.norm(got - ref, axis=-1) / np.linalg.norm(ref, axis=-1)
+        assert e.max() <= CHUNK_REL_L2, (b, h, e.max())
